@@ -15,6 +15,12 @@ tensors into its entry points:
     moe_pack_weights_mxfp8 quantised expert weights for the MXFP8 grouped GEMMs
                            (config(..., precision="mxfp8"))
     moe_mxfp8_quantize     MXFP8 quantisation of a bf16 matrix along its rows
+    moe_grouped_gemm       one product per expert over ragged groups with bias, activation
+                           and residual (_dgrad, _wgrad: its gradients)
+    moe_linear             the same for one dense weight (_dgrad, _wgrad)
+    moe_act_backward       gradient through an activation alone
+    moe_dropout            residual dropout, the mask drawn from a counter (its own backward)
+    moe_unpermute_combine_dropout  combine, dropout and residual in one pass
 """
 from ._lib import (  # noqa: F401
     EXPORTED, LIB_PATH, MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_ERR_CUDA, MOE_ERR_INVALID_ARG, MOE_ERR_NO_DEVICE,
@@ -28,4 +34,7 @@ from ._lib import (  # noqa: F401
     moe_grouped_ffn, moe_layer_backward, moe_layer_forward, moe_pack_weights, moe_pack_weights_backward,
     moe_permute, moe_permute_static_scratch, moe_route,
     moe_unpermute_combine, moe_workspace_size, moe_gemm_tiles_used, perm_rows, workspace,
-    moe_mxfp8_quantize, moe_mxfp8_weights_size, moe_pack_weights_mxfp8, mx_counters, mxfp8_scale_bytes)
+    moe_mxfp8_quantize, moe_mxfp8_weights_size, moe_pack_weights_mxfp8, mx_counters, mxfp8_scale_bytes,
+    MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_STATUS_BAD_OFFSETS, MoeGemmConfig,
+    moe_act_backward, moe_dropout, moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_linear,
+    moe_linear_dgrad, moe_linear_wgrad, moe_unpermute_combine_dropout)

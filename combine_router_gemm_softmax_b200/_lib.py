@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_NO_DEVICE = range(6)
 MOE_STATUS_NAN_LOGIT, MOE_STATUS_BAD_ROUTE, MOE_STATUS_TIMEOUT = 1, 2, 4
-MOE_STATUS_MX_SATURATED, MOE_STATUS_MX_UNDERFLOW = 8, 16
+MOE_STATUS_MX_SATURATED, MOE_STATUS_MX_UNDERFLOW, MOE_STATUS_BAD_OFFSETS = 8, 16, 32
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU = 0, 1, 2, 3, 4
 MOE_PRECISION_BF16, MOE_PRECISION_MXFP8 = 0, 1
 MOE_COMBINE_AUTO, MOE_COMBINE_SEPARATE, MOE_COMBINE_FUSED = 0, 1, 2
 MOE_PREACT_RECOMPUTE, MOE_PREACT_SAVE = 0, 1
@@ -35,7 +36,9 @@ EXPORTED = ("moe_workspace_size", "moe_status_string", "moe_version", "moe_pack_
             "moe_permute", "moe_grouped_ffn", "moe_unpermute_combine", "moe_layer_forward",
             "moe_permute_static_scratch", "moe_layer_forward_timed", "moe_pack_weights_backward",
             "moe_layer_backward", "moe_mxfp8_quantize", "moe_mxfp8_weights_size", "moe_pack_weights_mxfp8",
-            "moe_debug_stall_next_gemms", "moe_gemm_tiles_used")
+            "moe_debug_stall_next_gemms", "moe_gemm_tiles_used", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+            "moe_grouped_gemm_wgrad", "moe_linear", "moe_linear_dgrad", "moe_linear_wgrad", "moe_act_backward",
+            "moe_dropout", "moe_unpermute_combine_dropout")
 
 
 class MoeError(RuntimeError):
@@ -59,6 +62,13 @@ class MoeConfig(ctypes.Structure):
         return torch.bfloat16 if self.dtype == MOE_DTYPE_BF16 else torch.float32
 
 
+class MoeGemmConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("ldz", ctypes.c_int64)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -66,6 +76,10 @@ P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
 CFG = ctypes.POINTER(MoeConfig)
+GCFG = ctypes.POINTER(MoeGemmConfig)
+I64 = ctypes.c_int64
+U64 = ctypes.c_uint64
+F64 = ctypes.c_double
 
 _SIGS = {
     "moe_workspace_size": (SZ, [CFG, I32]),
@@ -86,6 +100,15 @@ _SIGS = {
     "moe_mxfp8_weights_size": (SZ, [CFG, I32]),
     "moe_pack_weights_mxfp8": (I32, [CFG, P, P, P, P, P, P]),
     "moe_debug_stall_next_gemms": (I32, [I32]),
+    "moe_grouped_gemm": (I32, [GCFG, P, P, P, P, P, P, P, P, P]),
+    "moe_grouped_gemm_dgrad": (I32, [GCFG, P, P, P, P, P, P, P, P]),
+    "moe_grouped_gemm_wgrad": (I32, [GCFG, P, P, P, P, P, P, P]),
+    "moe_linear": (I32, [GCFG, P, P, P, P, P, P, P, P]),
+    "moe_linear_dgrad": (I32, [GCFG, P, P, P, P, P, P, P]),
+    "moe_linear_wgrad": (I32, [GCFG, P, P, P, P, P, P]),
+    "moe_act_backward": (I32, [GCFG, P, P, P, P]),
+    "moe_dropout": (I32, [I32, I32, I32, P, I64, P, I64, P, I64, F64, P, U64, P]),
+    "moe_unpermute_combine_dropout": (I32, [CFG, P, P, P, P, F64, P, U64, P, P]),
 }
 
 
@@ -433,3 +456,273 @@ def mx_counters(ws):
     """The four uint32 counters an MXFP8 call leaves at the start of its
     workspace: x saturated, x underflowed, h_mid saturated, h_mid underflowed."""
     return ws[:16].view(torch.int32).cpu().tolist()
+
+
+# ------------------------------------------------------------------ free products and dropout
+
+_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH,
+         "silu": MOE_ACT_SILU}
+_GEMM_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _act(act) -> int:
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"act: {act!r} is none of {', '.join(_ACTS)}") from None
+
+
+def _strided(t, shape, dtype, device, name):
+    """Checks a matrix whose rows may lie apart (unit stride along the last
+    axis) and returns its address and row stride; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    st = t.stride()
+    rows, width = shape[-2], shape[-1]
+    ld = st[-2] if rows > 1 else (width + 7) // 8 * 8  # a single row's stride leads nowhere
+    if (width > 1 and st[-1] != 1) or ld < width:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {st})")
+    return t.data_ptr(), ld
+
+
+def _matrix(rows, width, dtype, device):
+    """A new matrix whose rows start on 16 bytes (odd widths get padded rows)."""
+    wide = (width + 7) // 8 * 8
+    t = torch.empty((rows, wide), dtype=dtype, device=device)
+    return t if wide == width else t[:, :width]
+
+
+def _plain(t, shape, dtype, device, name):
+    """Address of a contiguous tensor of this shape; None for None."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _first(t, dims, name):
+    """Device and MOE_DTYPE_* of a call's leading operand."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be on a CUDA device")
+    if t.dim() != dims:
+        raise ValueError(f"{name}: {t.dim()} axes, not {dims}")
+    try:
+        return t.device, _GEMM_DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32") from None
+
+
+def _enqueue(fn, device, stream, *args):
+    """Calls the entry point on `stream` (default: the device's current one),
+    with the tensors' device current."""
+    f = getattr(_lib or lib(), fn)
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = f(*args, raw)
+    if code != MOE_OK:
+        _rc(fn, code)
+
+
+def _weights(w, groups, n, k, dtype, device):
+    """Address, row stride and group stride of w [groups, n, k] (or [n, k])."""
+    p, ld = _strided(w, (groups, n, k) if w.dim() == 3 else (n, k), dtype, device, "w")
+    if w.dim() == 2 or groups <= 1:
+        return p, ld, n * ld
+    between = w.stride(0)
+    if between < (n - 1) * ld + k:
+        raise ValueError(f"w: groups must not overlap (strides {w.stride()})")
+    return p, ld, between
+
+
+def _forward(fn, x, offsets, w, bias, act, residual, preact, y, status, stream):
+    dev, dt = _first(x, 2, "x")
+    _first(w, 2 if fn == "moe_linear" else 3, "w")
+    rows, k = x.shape
+    n = w.shape[-2]
+    groups = w.shape[0] if w.dim() == 3 else 1
+    tdt = x.dtype
+    px, ldx = _strided(x, (rows, k), tdt, dev, "x")
+    pw, ldw, ws = _weights(w, groups, n, k, tdt, dev)
+    pb = _plain(bias, w.shape[:-1], torch.float32, dev, "bias")
+    pr, ldr = _strided(residual, (rows, n), tdt, dev, "residual")
+    pz, ldz = _strided(preact, (rows, n), tdt, dev, "preact")
+    if y is None:
+        y = _matrix(rows, n, tdt, dev)
+    py, ldy = _strided(y, (rows, n), tdt, dev, "y")
+    cfg = MoeGemmConfig(rows, n, k, groups, dt, _act(act), ldx, ldw, ws, ldy, ldr, ldz)
+    ps = _plain(status, (1,), torch.int32, dev, "status")
+    if fn == "moe_linear":
+        _enqueue(fn, dev, stream, cfg, px, pw, pb, pr, pz, py, ps)
+    else:
+        _enqueue(fn, dev, stream, cfg, px, _plain(offsets, (groups + 1,), torch.int32, dev, "offsets"), pw, pb, pr, pz,
+                 py, ps)
+    return y
+
+
+def _dgrad(fn, dy, offsets, w, z, act, residual, dx, status, stream):
+    dev, dt = _first(dy, 2, "dy")
+    _first(w, 2 if fn == "moe_linear_dgrad" else 3, "w")
+    rows, n = dy.shape
+    k = w.shape[-1]
+    groups = w.shape[0] if w.dim() == 3 else 1
+    tdt = dy.dtype
+    pdy, ldy = _strided(dy, (rows, n), tdt, dev, "dy")
+    pw, ldw, ws = _weights(w, groups, n, k, tdt, dev)
+    pz, ldz = _strided(z, (rows, k), tdt, dev, "z")
+    pr, ldr = _strided(residual, (rows, k), tdt, dev, "residual")
+    if dx is None:
+        dx = _matrix(rows, k, tdt, dev)
+    pdx, ldx = _strided(dx, (rows, k), tdt, dev, "dx")
+    cfg = MoeGemmConfig(rows, n, k, groups, dt, _act(act), ldx, ldw, ws, ldy, ldr, ldz)
+    ps = _plain(status, (1,), torch.int32, dev, "status")
+    if fn == "moe_linear_dgrad":
+        _enqueue(fn, dev, stream, cfg, pdy, pw, pz, pr, pdx, ps)
+    else:
+        _enqueue(fn, dev, stream, cfg, pdy, _plain(offsets, (groups + 1,), torch.int32, dev, "offsets"), pw, pz, pr,
+                 pdx, ps)
+    return dx
+
+
+def _wgrad(fn, dy, offsets, x, groups, dw, dbias, status, stream):
+    dev, dt = _first(dy, 2, "dy")
+    rows, n = dy.shape
+    _first(x, 2, "x")
+    k = x.shape[1]
+    pdy, ldy = _strided(dy, (rows, n), dy.dtype, dev, "dy")
+    px, ldx = _strided(x, (rows, k), dy.dtype, dev, "x")
+    dense = fn == "moe_linear_wgrad"
+    shape = (n, k) if dense else (groups, n, k)
+    if dw is None:
+        dw = torch.empty(shape, dtype=torch.float32, device=dev)
+    pdw = _plain(dw, shape, torch.float32, dev, "dw")
+    pdb = _plain(dbias, shape[:-1], torch.float32, dev, "dbias")
+    cfg = MoeGemmConfig(rows, n, k, groups, dt, MOE_ACT_NONE, ldx, 0, 0, ldy, 0, 0)
+    ps = _plain(status, (1,), torch.int32, dev, "status")
+    if dense:
+        _enqueue(fn, dev, stream, cfg, pdy, px, pdw, pdb, ps)
+    else:
+        _enqueue(fn, dev, stream, cfg, pdy, _plain(offsets, (groups + 1,), torch.int32, dev, "offsets"), px, pdw, pdb,
+                 ps)
+    return dw
+
+
+def moe_grouped_gemm(x, offsets, w, bias=None, act="none", residual=None, preact=None, y=None, status=None,
+                     stream=None):
+    """y[r] = act(x[r] w[e]^T + bias[e]) + residual[r] for the rows r in
+    [offsets[e], offsets[e+1]) of each expert e. x [rows, k], offsets [E+1]
+    int32 on the device (as moe_permute writes them), w [E, n, k], bias [E, n]
+    fp32; act "none", "relu", "gelu", "gelu_tanh" or "silu"; preact [rows, n]
+    receives the argument of act. Rows of matrices may lie apart (bf16 row
+    strides: multiples of 8). Rows outside every group are left as they were
+    (uninitialised in a y made here). Returns y."""
+    return _forward("moe_grouped_gemm", x, _given(offsets), w, bias, act, residual, preact, y, status, stream)
+
+
+def moe_grouped_gemm_dgrad(dy, offsets, w, z=None, act="none", residual=None, dx=None, status=None, stream=None):
+    """dx[r] = act'(z[r]) * (dy[r] w[e]) + residual[r]: the input gradient,
+    through the activation x = act(z) that made the input when z [rows, k] is
+    given. Returns dx [rows, k]."""
+    return _dgrad("moe_grouped_gemm_dgrad", dy, _given(offsets), w, z, act, residual, dx, status, stream)
+
+
+def moe_grouped_gemm_wgrad(dy, offsets, x, dw=None, dbias=None, status=None, stream=None):
+    """dw[e] = dy_e^T x_e (fp32 [E, n, k], E from offsets); dbias [E, n] fp32,
+    when given, receives the column sums of dy_e. Returns dw."""
+    return _wgrad("moe_grouped_gemm_wgrad", dy, _given(offsets), x, offsets.numel() - 1, dw, dbias, status, stream)
+
+
+def moe_linear(x, w, bias=None, act="none", residual=None, preact=None, y=None, status=None, stream=None):
+    """y = act(x w^T + bias) + residual for one dense weight w [n, k]; the
+    arguments are moe_grouped_gemm's. Returns y [rows, n]."""
+    return _forward("moe_linear", x, None, w, bias, act, residual, preact, y, status, stream)
+
+
+def moe_linear_dgrad(dy, w, z=None, act="none", residual=None, dx=None, status=None, stream=None):
+    """dx = act'(z) * (dy w) + residual, see moe_grouped_gemm_dgrad."""
+    return _dgrad("moe_linear_dgrad", dy, None, w, z, act, residual, dx, status, stream)
+
+
+def moe_linear_wgrad(dy, x, dw=None, dbias=None, status=None, stream=None):
+    """dw = dy^T x (fp32 [n, k]) and, when dbias [n] is given, the column sums
+    of dy. Returns dw."""
+    return _wgrad("moe_linear_wgrad", dy, None, x, 1, dw, dbias, status, stream)
+
+
+def _given(offsets):
+    if offsets is None:
+        raise TypeError("offsets: expected a torch.Tensor")
+    return offsets
+
+
+def moe_act_backward(dy, z, act, dz=None, stream=None):
+    """dz = dy * act'(z) over [rows, n], for an activation that no further
+    product consumes. Returns dz (which may be dy)."""
+    dev, dt = _first(dy, 2, "dy")
+    shape = dy.shape
+    pdy, ldy = _strided(dy, shape, dy.dtype, dev, "dy")
+    pz, ldz = _strided(z, shape, dy.dtype, dev, "z")
+    if dz is None:
+        dz = _matrix(*shape, dy.dtype, dev)
+    pdz, ldr = _strided(dz, shape, dy.dtype, dev, "dz")
+    cfg = MoeGemmConfig(shape[0], shape[1], 1, 1, dt, _act(act), 0, 0, 0, ldy, ldr, ldz)
+    _enqueue("moe_act_backward", dev, stream, cfg, pdy, pz, pdz)
+    return dz
+
+
+def moe_dropout(x, p, rng=None, offset=0, residual=None, y=None, stream=None):
+    """y = residual + dropout(x) over a matrix [rows, cols], bf16 or fp32. rng:
+    int64 [2] on the device (seed, counter offset), added to the host's
+    `offset`; the mask is a function of them and of the element's place, so
+    moe_dropout(dy, p, rng, offset) is the backward. Returns y (which may be x
+    or residual)."""
+    dev, dt = _first(x, 2, "x")
+    shape = x.shape
+    px, ldx = _strided(x, shape, x.dtype, dev, "x")
+    pr, ldr = _strided(residual, shape, x.dtype, dev, "residual")
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
+    py, ldy = _strided(y, shape, x.dtype, dev, "y")
+    _enqueue("moe_dropout", dev, stream, shape[0], shape[1], dt, px, ldx, pr, ldr, py, ldy, p,
+             _plain(rng, (2,), torch.int64, dev, "rng"), offset)
+    return y
+
+
+def moe_unpermute_combine_dropout(cfg, y_perm, dest_row, topk_gate, p, rng=None, offset=0, residual=None, y=None,
+                                  stream=None):
+    """y[t] = residual[t] + dropout(sum_j topk_gate[t, j] y_perm[dest_row[t, j]]):
+    moe_unpermute_combine and moe_dropout in one pass, the sum not rounded in
+    between. Returns y [T, d] (which may be residual)."""
+    dev, _ = _first(y_perm, 2, "y_perm")
+    dt = cfg.torch_dtype
+    rows = max(perm_rows(cfg), 1)
+    if y_perm.shape[0] < perm_rows(cfg) or y_perm.shape[1] != cfg.d:
+        raise ValueError(f"y_perm: shape {tuple(y_perm.shape)}, needs {rows} rows of {cfg.d}")
+    pp = _plain(y_perm, y_perm.shape, dt, dev, "y_perm")
+    pd = _plain(dest_row, (cfg.T, cfg.k), torch.int32, dev, "dest_row")
+    pg = _plain(topk_gate, (cfg.T, cfg.k), torch.float32, dev, "topk_gate")
+    pr = _plain(residual, (cfg.T, cfg.d), dt, dev, "residual")
+    if y is None:
+        y = torch.empty((cfg.T, cfg.d), dtype=dt, device=dev)
+    py = _plain(y, (cfg.T, cfg.d), dt, dev, "y")
+    _enqueue("moe_unpermute_combine_dropout", dev, stream, cfg, pp, pd, pg, pr, p,
+             _plain(rng, (2,), torch.int64, dev, "rng"), offset, py)
+    return y

@@ -22,12 +22,6 @@ int device_sm_count() {
   return n;
 }
 
-namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
@@ -41,6 +35,8 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // Row-major bf16 matrix [rows, cols], box of box_rows x 64 columns, 128-byte swizzle.
 int make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
@@ -521,7 +517,7 @@ using namespace moe;
 
 extern "C" {
 
-int32_t moe_version(void) { return (1 << 16) | 2; }
+int32_t moe_version(void) { return (1 << 16) | 3; }
 
 int32_t moe_gemm_tiles_used(const moe_config* cfg, int32_t* tiles) {
   if (tiles == nullptr) return MOE_ERR_INVALID_ARG;

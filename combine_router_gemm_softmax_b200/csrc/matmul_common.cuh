@@ -1,0 +1,194 @@
+// What the kernels of the free products (moe_grouped_gemm, moe_linear and
+// their gradients) share: the argument block, the ragged row groups, the
+// activations with their derivatives, and the epilogue of one output element.
+//
+//   rows mode    D[r, n] = fin( sum_k A[r, k] B_e[., .] ), r in group e's rows.
+//                Forward: A = x, B_e = W_e [N, K]. Input gradient: A = dy,
+//                B_e = W_e read across (its rows are the reduction).
+//   weight mode  D_e[m, n] = sum_{r in group e} A[r, m] B[r, n] (A = dy, B = x).
+#pragma once
+
+#include "moe_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+// Rows of group e: [offsets[e], offsets[e+1]) held inside [0, rows], so that
+// no offset the caller passes leads outside the buffers; one group of all
+// rows without offsets. The bounds may be clamped, which the kernels report
+// as MOE_STATUS_BAD_OFFSETS.
+MOE_DEV int2 group_rows(const int32_t* offsets, int e, int rows, bool* bad = nullptr) {
+  if (offsets == nullptr) return make_int2(0, rows);
+  const int a = offsets[e], b = offsets[e + 1];
+  const int r0 = min(max(a, 0), rows), r1 = min(max(b, r0), rows);
+  if (bad != nullptr && (r0 != a || r1 != b)) *bad = true;
+  return make_int2(r0, r1);
+}
+
+// One warp: s_rows[e] = group e's rows, prefix[e] = row tiles (of 2^tile_shift rows)
+// before group e, prefix[E] = all of them. E <= kMaxE (eight groups a lane).
+MOE_DEV void build_groups(const int32_t* offsets, int E, int rows, int tile_shift, int2* s_rows, int* prefix,
+                          int32_t* status, int lane) {
+  int loc[kMaxE / 32];
+  int sum = 0;
+  bool bad = false;
+#pragma unroll
+  for (int v = 0; v < kMaxE / 32; ++v) {
+    const int e = lane * (kMaxE / 32) + v;
+    loc[v] = 0;
+    if (e < E) {
+      const int2 r = group_rows(offsets, e, rows, &bad);
+      s_rows[e] = r;
+      loc[v] = (r.y - r.x + (1 << tile_shift) - 1) >> tile_shift;
+    }
+    sum += loc[v];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  int run = inc - sum;
+#pragma unroll
+  for (int v = 0; v < kMaxE / 32; ++v) {
+    const int e = lane * (kMaxE / 32) + v;
+    if (e < E) prefix[e] = run;
+    run += loc[v];
+  }
+  if (lane == 31) prefix[E] = inc;
+  if (bad && blockIdx.x == 0) report_status(status, MOE_STATUS_BAD_OFFSETS);
+}
+
+// The group that row tile t belongs to: prefix[e] <= t < prefix[e+1].
+MOE_DEV int group_of_tile(const int* prefix, int E, int t) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ activations
+// Phi, the standard normal distribution function, by Abramowitz and Stegun
+// 7.1.26: erfc(t) = p(s) exp(-t^2), s = 1 / (1 + 0.3275911 t), absolute error
+// at most 1.5e-7, and gauss = exp(-z^2 / 2). For results that are rounded to
+// bf16 next.
+MOE_DEV float phi_fast(float z, float& gauss) {
+  const float t = fabsf(z) * 0.70710678f;
+  const float s = __fdividef(1.0f, fmaf(0.3275911f, t, 1.0f));
+  gauss = __expf(-t * t);
+  float p = fmaf(1.061405429f, s, -1.453152027f);
+  p = fmaf(p, s, 1.421413741f);
+  p = fmaf(p, s, -0.284496736f);
+  p = fmaf(p, s, 0.254829592f);
+  const float tail = 0.5f * p * s * gauss;  // Phi(-|z|)
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// kFast: the fast exponential, reciprocal and phi_fast (about 1e-6 relative,
+// or absolute in Phi), for outputs rounded to bf16; else the IEEE forms, for
+// fp32 outputs.
+template <bool kFast>
+MOE_DEV float sigmoid_of(float z) {
+  // __fdividef returns 0 for divisors above 2^126 (z < -87): below every bf16 product of interest
+  return kFast ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
+}
+
+constexpr float kGeluTanhC = 0.7978845608028654f;  // sqrt(2 / pi)
+
+// The tanh form of GELU is z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3),
+// since (1 + tanh u) / 2 = sigmoid(2 u): no cancellation for negative z.
+template <bool kFast>
+MOE_DEV float act_of(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU:
+      return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case MOE_ACT_GELU: {
+      float gauss;
+      // erfc keeps its relative precision in the negative tail
+      return z * (kFast ? phi_fast(z, gauss) : 0.5f * erfcf(-z * 0.70710678118654752f));
+    }
+    case MOE_ACT_GELU_TANH:
+      return z * sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
+    case MOE_ACT_SILU:
+      return z * sigmoid_of<kFast>(z);
+    default:
+      return z;
+  }
+}
+
+template <bool kFast>
+MOE_DEV float act_slope(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU:
+      return z > 0.0f ? 1.0f : 0.0f;
+    case MOE_ACT_GELU: {
+      float gauss, phi;
+      if (kFast) {
+        phi = phi_fast(z, gauss);
+      } else {
+        phi = 0.5f * erfcf(-z * 0.70710678118654752f);
+        gauss = expf(-0.5f * z * z);
+      }
+      return fmaf(z * 0.3989422804014327f, gauss, phi);
+    }
+    case MOE_ACT_GELU_TANH: {
+      const float s = sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
+      const float du = 2.0f * kGeluTanhC * (1.0f + 3.0f * 0.044715f * z * z);
+      return fmaf(z * s * (1.0f - s), du, s);
+    }
+    case MOE_ACT_SILU: {
+      const float s = sigmoid_of<kFast>(z);
+      return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    default:
+      return 1.0f;
+  }
+}
+
+// ------------------------------------------------------------------ storage types
+template <typename T>
+MOE_DEV float to_f32(T v);
+template <>
+MOE_DEV float to_f32<float>(float v) {
+  return v;
+}
+template <>
+MOE_DEV float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <typename T>
+MOE_DEV T from_f32(float v);
+template <>
+MOE_DEV float from_f32<float>(float v) {
+  return v;
+}
+template <>
+MOE_DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// One output element of rows mode from its sum: forward
+// act(sum + bias) + residual (the pre-activation stored first), input
+// gradient sum * act'(z) + residual; rounded once.
+template <typename T, bool kDgrad>
+MOE_DEV void finish_element(const MatmulArgs& a, float sum, int e, long long r, int n) {
+  constexpr bool kFast = sizeof(T) == 2;
+  float v = sum;
+  if constexpr (kDgrad) {
+    if (a.z != nullptr) v *= act_slope<kFast>(to_f32(static_cast<const T*>(a.z)[r * a.ldz + n]), a.act);
+  } else {
+    if (a.bias != nullptr) v += a.bias[static_cast<size_t>(e) * a.n + n];
+    if (a.preact != nullptr) static_cast<T*>(a.preact)[r * a.ldz + n] = from_f32<T>(v);
+    v = act_of<kFast>(v, a.act);
+  }
+  if (a.residual != nullptr) v += to_f32(static_cast<const T*>(a.residual)[r * a.ldr + n]);
+  static_cast<T*>(a.d)[r * a.ldd + n] = from_f32<T>(v);
+}
+
+}  // namespace moe

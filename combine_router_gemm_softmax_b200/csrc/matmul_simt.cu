@@ -1,0 +1,388 @@
+// The free products in fp32 (moe_grouped_gemm, moe_linear and their
+// gradients with dtype MOE_DTYPE_F32), on the CUDA cores: products and sums
+// stay IEEE fp32, which the tensor cores' reduced input formats would not.
+//
+// A CTA of 256 threads owns a tile of BT x BT outputs (BT 128 or 64), each
+// thread (BT/16)^2 of them in registers as pairs along n, so that one packed
+// fma.rn.f32x2 does two multiply-adds. Slices of 16 along the reduction pass
+// through two shared-memory buffers; the next slice is in flight in registers
+// while this one is multiplied. Operands are read as they lie: along the
+// reduction or across it, by template, so no mode needs a transposed copy.
+// Bound: the fp32 pipe (128 multiply-adds a cycle and SM).
+//
+// Few tiles leave SMs idle, so a cluster of S CTAs can share one 64 x 64 tile:
+// each takes a part of the reduction, and the partial tiles are added through
+// distributed shared memory in the order of the CTAs' ranks (the same sum on
+// every run).
+#include "matmul_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 16;
+constexpr int kThreads = 256;
+
+struct Quad {
+  float v[4];
+};
+
+// Four elements from p, `valid` of them inside the row (the others zero).
+template <typename T>
+MOE_DEV Quad load4(const T* p, int valid, bool vec) {
+  Quad q;
+  if (valid >= 4 && vec) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p);
+      q.v[0] = f.x, q.v[1] = f.y, q.v[2] = f.z, q.v[3] = f.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+      const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+      q.v[0] = lo.x, q.v[1] = lo.y, q.v[2] = hi.x, q.v[3] = hi.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q.v[j] = j < valid ? to_f32(p[j]) : 0.0f;
+  }
+  return q;
+}
+
+// One operand's slice of BT (rows of the tile) x 16 (reduction), in registers.
+// kAlong: elements lie along the reduction (row-major tile rows); else across.
+template <typename T, bool kAlong, int BT>
+struct Slice {
+  static constexpr int kQuads = BT * kBK / 4 / kThreads;
+  Quad q[kQuads];
+
+  // base: element (first row of the tile, reduction index 0); rows and
+  // depth: what of the tile and of the reduction [k0, ...) exists.
+  MOE_DEV void load(const T* base, long long ld, int rows, int k0, int depth, bool vec) {
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      const int id = threadIdx.x + i * kThreads;
+      if constexpr (kAlong) {
+        const int r = id >> 2, k = k0 + (id & 3) * 4;
+        q[i] = load4(base + r * ld + k, r < rows ? depth - k : 0, vec);
+      } else {
+        const int k = k0 + id / (BT / 4), r = (id % (BT / 4)) * 4;
+        q[i] = load4(base + k * ld + r, k < depth ? rows - r : 0, vec);
+      }
+    }
+  }
+
+  MOE_DEV void store(float (*s)[BT + 4]) const {
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      const int id = threadIdx.x + i * kThreads;
+      if constexpr (kAlong) {
+        const int r = id >> 2, k = (id & 3) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[k + j][r] = q[i].v[j];
+      } else {
+        const int k = id / (BT / 4), r = (id % (BT / 4)) * 4;
+        *reinterpret_cast<float4*>(&s[k][r]) = make_float4(q[i].v[0], q[i].v[1], q[i].v[2], q[i].v[3]);
+      }
+    }
+  }
+};
+
+MOE_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+MOE_DEV void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+MOE_DEV float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+// BT x BT outputs of a thread grid of 16 x 16: row i of thread ty is
+// (i / 4) * (BT / 2) + ty * 4 + i % 4 for BT 128 (two groups of four), ty * 4 + i for 64.
+template <int BT>
+MOE_DEV int at(int t, int i) {
+  return BT == 128 ? (i >> 2) * 64 + t * 4 + (i & 3) : t * 4 + i;
+}
+
+template <typename T, MatmulMode kMode, int BT>
+__global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs a) {
+  constexpr int kPer = BT / 16;  // outputs of a thread along each axis
+  constexpr bool kWeight = kMode == MatmulMode::kWgrad;
+  __shared__ __align__(16) float sA[2][kBK][BT + 4];
+  __shared__ __align__(16) float sB[2][kBK][BT + 4];
+  __shared__ int2 s_rows[kMaxE];
+  __shared__ int prefix[kMaxE + 1];
+  // a partial tile for the sum over the cluster (64 x 64 only)
+  __shared__ __align__(16) float s_part[BT == 64 ? 64 * 64 : 4];
+
+  uint32_t split, part;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+  part = split > 1 ? cluster_ctarank() : 0;
+  if (threadIdx.x < 32)
+    build_groups(a.offsets, a.groups, a.rows, BT == 128 ? 7 : 6, s_rows, prefix, a.status, threadIdx.x);
+  __syncthreads();
+  const int tiles_n = (a.n + BT - 1) / BT;
+  const int tiles_m = kWeight ? (a.m + BT - 1) / BT : prefix[a.groups];
+  const long long total = static_cast<long long>(tiles_n) * tiles_m * (kWeight ? a.groups : 1);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+
+  for (long long tile = blockIdx.x / split; tile < total; tile += gridDim.x / split) {
+    const int tn = static_cast<int>(tile % tiles_n);
+    const long long rest = tile / tiles_n;
+    int e, m0, m_valid, depth, k_first = 0;
+    const int n0 = tn * BT, n_valid = min(BT, a.n - n0);
+    const T* pa;
+    const T* pb;
+    if constexpr (kWeight) {
+      e = static_cast<int>(rest / tiles_m);
+      m0 = static_cast<int>(rest % tiles_m) * BT;
+      m_valid = min(BT, a.m - m0);
+      depth = s_rows[e].y - s_rows[e].x;
+      pa = static_cast<const T*>(a.a) + s_rows[e].x * a.lda + m0;
+      pb = static_cast<const T*>(a.b) + s_rows[e].x * a.ldb + n0;
+    } else {
+      e = group_of_tile(prefix, a.groups, static_cast<int>(rest));
+      m0 = s_rows[e].x + (static_cast<int>(rest) - prefix[e]) * BT;
+      m_valid = min(BT, s_rows[e].y - m0);
+      depth = a.k;
+      pa = static_cast<const T*>(a.a) + m0 * a.lda;
+      pb = static_cast<const T*>(a.b) + e * a.b_stride + (kMode == MatmulMode::kForward ? n0 * a.ldb : n0);
+    }
+    if (split > 1) {
+      const int slices = (depth + kBK - 1) / kBK;
+      k_first = static_cast<int>(static_cast<long long>(slices) * part / split) * kBK;
+      depth = min(depth, static_cast<int>(static_cast<long long>(slices) * (part + 1) / split) * kBK);
+    }
+
+    uint64_t acc[kPer][kPer / 2];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+      for (int j = 0; j < kPer / 2; ++j) acc[i][j] = 0;
+
+    Slice<T, !kWeight, BT> qa;
+    Slice<T, kMode == MatmulMode::kForward, BT> qb;
+    if (k_first < depth) {
+      qa.load(pa, a.lda, m_valid, k_first, depth, a.vec_a);
+      qb.load(pb, a.ldb, n_valid, k_first, depth, a.vec_b);
+      qa.store(sA[0]);
+      qb.store(sB[0]);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int k0 = k_first; k0 < depth; k0 += kBK, buf ^= 1) {
+      const bool more = k0 + kBK < depth;
+      if (more) {
+        qa.load(pa, a.lda, m_valid, k0 + kBK, depth, a.vec_a);
+        qb.load(pb, a.ldb, n_valid, k0 + kBK, depth, a.vec_b);
+      }
+#pragma unroll
+      for (int k = 0; k < kBK; ++k) {
+        float ra[kPer];
+        uint64_t rb[kPer / 2];
+#pragma unroll
+        for (int g = 0; g < kPer / 4; ++g) {
+          const float4 f = *reinterpret_cast<const float4*>(&sA[buf][k][at<BT>(ty, g * 4)]);
+          ra[4 * g] = f.x, ra[4 * g + 1] = f.y, ra[4 * g + 2] = f.z, ra[4 * g + 3] = f.w;
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sB[buf][k][at<BT>(tx, g * 4)]);
+          rb[2 * g] = u.x, rb[2 * g + 1] = u.y;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const uint64_t d = pack2(ra[i], ra[i]);
+#pragma unroll
+          for (int j = 0; j < kPer / 2; ++j) fma2(acc[i][j], d, rb[j]);
+        }
+      }
+      if (more) {
+        qa.store(sA[buf ^ 1]);
+        qb.store(sB[buf ^ 1]);
+      }
+      __syncthreads();
+    }
+
+    auto finish = [&](int i, int j, float v) {
+      if (i >= m_valid || j >= n_valid) return;
+      if constexpr (kWeight)
+        static_cast<float*>(a.d)[(static_cast<long long>(e) * a.m + m0 + i) * a.ldd + n0 + j] = v;
+      else
+        finish_element<T, kMode == MatmulMode::kDgrad>(a, v, e, m0 + i, n0 + j);
+    };
+    if (BT == 64 && split > 1) {
+      // partial tiles side by side in the cluster's shared memory, each CTA
+      // adding and finishing its share of the rows
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j)
+          *reinterpret_cast<float2*>(&s_part[at<BT>(ty, i) * 64 + at<BT>(tx, 2 * j)]) = unpack2(acc[i][j]);
+      cluster_sync();
+      const uint32_t mine = smem_addr(s_part);
+      const int first = 64 * 64 / 4 * part / split, last = 64 * 64 / 4 * (part + 1) / split;
+      for (int q = first + threadIdx.x; q < last; q += kThreads) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t c = 0; c < split; ++c) {
+          float f[4];
+          ld_shared_cluster_v4(mapa_shared(mine + q * 16, c), f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[x] += f[x];
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) finish(q >> 4, (q & 15) * 4 + x, s[x]);
+      }
+      cluster_sync();  // nobody overwrites or leaves while a peer still reads
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+          const float2 f = unpack2(acc[i][j]);
+          finish(at<BT>(ty, i), at<BT>(tx, 2 * j), f.x);
+          finish(at<BT>(ty, i), at<BT>(tx, 2 * j + 1), f.y);
+        }
+    }
+  }
+}
+
+template <typename T, MatmulMode kMode>
+cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
+  const int sms = device_sm_count();
+  // no more than these row tiles exist, however the rows fall to the groups
+  auto tiles = [&](long long bt) {
+    const long long tn = (a.n + bt - 1) / bt;
+    const long long tm = kMode == MatmulMode::kWgrad ? static_cast<long long>(a.groups) * ((a.m + bt - 1) / bt)
+                                                     : a.rows / bt + a.groups;
+    return tm * tn;
+  };
+  if (tiles(128) >= sms)
+    return launch_kernel(matmul_simt_kernel<T, kMode, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
+                         dim3(kThreads), 0, s, false, 1, a);
+  const long long t = tiles(64);
+  const int depth = kMode == MatmulMode::kWgrad ? a.rows : a.k;
+  int split = 1;
+  while (split < 8 && t * split * 2 <= 2 * sms && depth / (split * 2) >= 64) split *= 2;
+  const long long grid = std::min<long long>(t, 4 * sms) * split;
+  return launch_kernel(matmul_simt_kernel<T, kMode, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, false,
+                       static_cast<unsigned>(split), a);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_matmul_simt(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+  switch (mode) {
+    case MatmulMode::kForward:
+      return launch_mode<T, MatmulMode::kForward>(a, s);
+    case MatmulMode::kDgrad:
+      return launch_mode<T, MatmulMode::kDgrad>(a, s);
+    default:
+      return launch_mode<T, MatmulMode::kWgrad>(a, s);
+  }
+}
+
+cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+  return launch_matmul_simt<float>(mode, a, s);
+}
+
+cudaError_t launch_matmul_bf16_simt(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+  return launch_matmul_simt<__nv_bfloat16>(mode, a, s);
+}
+
+// ------------------------------------------------------------------ bias gradient
+// db[e, n] = sum of dy[r, n] over group e's rows. A CTA of 256 threads takes
+// 8 warps x 32 lanes of four columns each; the cluster's CTAs share the rows,
+// and their sums meet in distributed shared memory in rank order.
+// Bound: HBM (dy read once).
+namespace {
+
+template <typename T>
+__global__ void __launch_bounds__(256) column_sum_kernel(const T* dy, long long ld, const int32_t* offsets, int rows,
+                                                         int n, float* out, int vec) {
+  __shared__ __align__(16) float s_sum[8][128];
+  uint32_t split, part;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+  part = split > 1 ? cluster_ctarank() : 0;
+  const int e = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n0 = static_cast<int>(blockIdx.x / split) * 128;
+  const int2 g = group_rows(offsets, e, rows);
+  const long long have = g.y - g.x;
+  const int r0 = g.x + static_cast<int>(have * part / split), r1 = g.x + static_cast<int>(have * (part + 1) / split);
+  const int c = n0 + lane * 4;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int r = r0 + warp; r < r1; r += 8) {
+    const Quad q = load4(dy + static_cast<long long>(r) * ld + c, n - c, vec != 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += q.v[j];
+  }
+  *reinterpret_cast<float4*>(&s_sum[warp][lane * 4]) = make_float4(s[0], s[1], s[2], s[3]);
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s_sum[w][threadIdx.x];
+    s_sum[0][threadIdx.x] = t;
+  }
+  if (split > 1) cluster_sync();
+  if (part == 0 && threadIdx.x < 128 && n0 + static_cast<int>(threadIdx.x) < n) {
+    float t = s_sum[0][threadIdx.x];
+    for (uint32_t p = 1; p < split; ++p) t += ld_shared_cluster_f32(mapa_shared(smem_addr(&s_sum[0][threadIdx.x]), p));
+    out[static_cast<size_t>(e) * n + n0 + threadIdx.x] = t;
+  }
+  if (split > 1) cluster_sync();
+}
+
+template <typename T>
+cudaError_t column_sums(const void* dy, long long ld, const int32_t* offsets, int groups, int rows, int n, float* out,
+                        bool vec, cudaStream_t s) {
+  const int blocks = (n + 127) / 128;
+  int split = 1;
+  while (split < 8 && static_cast<long long>(blocks) * groups * split < 4LL * device_sm_count()) split *= 2;
+  return launch_kernel(column_sum_kernel<T>, dim3(blocks * split, groups), dim3(256), 0, s, false,
+                       static_cast<unsigned>(split), static_cast<const T*>(dy), ld, offsets, rows, n, out,
+                       static_cast<int>(vec));
+}
+
+// dz = dy act'(z), elementwise over [rows, n]. Bound: HBM.
+template <typename T>
+__global__ void __launch_bounds__(256) act_backward_kernel(const T* dy, long long ldy, const T* z, long long ldz, T* dz,
+                                                           long long ldd, int rows, int n, int act, int vec) {
+  const int quads = (n + 3) / 4;
+  const long long total = static_cast<long long>(rows) * quads;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long r = i / quads;
+    const int c = static_cast<int>(i - r * quads) * 4;
+    const Quad q = load4(dy + r * ldy + c, n - c, vec != 0), w = load4(z + r * ldz + c, n - c, vec != 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < n) dz[r * ldd + c + j] = from_f32<T>(q.v[j] * act_slope<sizeof(T) == 2>(w.v[j], act));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const int32_t* offsets, int groups, int rows,
+                               int n, float* out, bool vec, cudaStream_t s) {
+  return dtype == MOE_DTYPE_F32 ? column_sums<float>(dy, ld, offsets, groups, rows, n, out, vec, s)
+                                : column_sums<__nv_bfloat16>(dy, ld, offsets, groups, rows, n, out, vec, s);
+}
+
+cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const void* z, long long ldz, void* dz,
+                                long long ldd, int rows, int n, int act, bool vec, cudaStream_t s) {
+  const long long quads = static_cast<long long>(rows) * ((n + 3) / 4);
+  const unsigned grid = static_cast<unsigned>(std::min<long long>((quads + 255) / 256, device_sm_count() * 16LL));
+  if (dtype == MOE_DTYPE_F32)
+    return launch_kernel(act_backward_kernel<float>, dim3(grid), dim3(256), 0, s, false, 1, static_cast<const float*>(dy),
+                         ldy, static_cast<const float*>(z), ldz, static_cast<float*>(dz), ldd, rows, n, act,
+                         static_cast<int>(vec));
+  return launch_kernel(act_backward_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, false, 1,
+                       static_cast<const __nv_bfloat16*>(dy), ldy, static_cast<const __nv_bfloat16*>(z), ldz,
+                       static_cast<__nv_bfloat16*>(dz), ldd, rows, n, act, static_cast<int>(vec));
+}
+
+}  // namespace moe

@@ -310,6 +310,20 @@ MOE_DEV void st_shared_cluster_v4(uint32_t cluster_saddr, uint32_t a, uint32_t b
                : "memory");
 }
 
+// Loads from another CTA's shared memory (16-byte aligned for v4).
+MOE_DEV void ld_shared_cluster_v4(uint32_t cluster_saddr, float (&f)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+               : "r"(cluster_saddr)
+               : "memory");
+}
+
+MOE_DEV float ld_shared_cluster_f32(uint32_t cluster_saddr) {
+  float f;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(cluster_saddr) : "memory");
+  return f;
+}
+
 // Tile load issued by each CTA of a pair into its own shared memory; the byte
 // count is credited to the barrier at `bar_cluster_saddr` (the leader's).
 MOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster_saddr, int x, int y) {

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/moe.h"
 
 namespace moe {
@@ -17,6 +19,12 @@ constexpr int kTileM = 128;
 constexpr int kGemmTileN = 256;
 
 int device_sm_count();
+
+// api.cu: the driver's tensor-map encoder (NULL where there is none).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
 
 // router.cu
 // Padded expert count of the router's score tile: a multiple of 16, or of 32
@@ -152,5 +160,47 @@ cudaError_t launch_transpose_grouped(const void* X, int C, const int32_t* offset
                                      int ppad_max, void* XT, cudaStream_t s);
 // [E][R][C] -> [E][C][R], bf16, R and C multiples of 64.
 cudaError_t launch_transpose_batched(const void* X, int E, int R, int C, void* XT, cudaStream_t s);
+
+
+// Dropout of one call: words below `cut` = floor(p 2^32) drop (0: keep all, rng unread).
+struct DropoutArgs {
+  const unsigned long long* rng;  // device: seed, offset
+  unsigned long long offset;
+  uint32_t cut;
+  float scale;  // 1 / (1 - p)
+};
+// dropout.cu
+cudaError_t launch_dropout(int dtype, int rows, int cols, const void* x, long long ldx, const void* residual,
+                           long long ldr, void* y, long long ldy, const DropoutArgs& d, cudaStream_t s);
+// dispatch.cu
+cudaError_t launch_combine_dropout(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate,
+                                   const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
+                                   cudaStream_t s);
+
+// The free products (matmul_common.cuh describes the modes). Strides in elements.
+enum class MatmulMode { kForward, kDgrad, kWgrad };
+struct MatmulArgs {
+  const void *a, *b;       // rows modes: x or dy, and W; weight mode: dy and x
+  const int32_t* offsets;  // [groups + 1], or NULL: one group of all rows
+  int groups, rows;        // rows of the ragged buffers
+  int m, n, k;             // columns of D; rows modes: k the reduction; weight mode: m rows of D_e
+  long long lda, ldb, b_stride, ldd;
+  const float* bias;       // [groups, n] or NULL
+  const void* z;           // kDgrad: pre-activations whose slope scales D, or NULL
+  void* preact;            // kForward: pre-activations out, or NULL
+  const void* residual;    // or NULL
+  long long ldz, ldr;      // ldz: z or preact
+  void* d;
+  int act;
+  int32_t* status;
+  int vec_a, vec_b;        // strides allow four-element loads (fp32 path)
+};
+// matmul_simt.cu
+cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+cudaError_t launch_matmul_bf16_simt(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const int32_t* offsets, int groups, int rows,
+                               int n, float* out, bool vec, cudaStream_t s);
+cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const void* z, long long ldz, void* dz,
+                                long long ldd, int rows, int n, int act, bool vec, cudaStream_t s);
 
 }  // namespace moe

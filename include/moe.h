@@ -15,7 +15,10 @@
  * routing map, a permutation that groups token rows by expert, the experts,
  * and the return of every output to its original token position. On one GPU
  * the dispatch and the return are on-device permutations. moe_layer_backward
- * differentiates the same layer (bf16, SwiGLU experts).
+ * differentiates the same layer (bf16, SwiGLU experts). Around the layer stand
+ * the free products (moe_grouped_gemm per expert, moe_linear dense, each with
+ * bias, activation and residual and its gradients) and residual dropout
+ * (moe_dropout, moe_unpermute_combine_dropout).
  *
  * Conventions for every entry point:
  *  - Tensor arguments are DEVICE pointers owned by the caller. The library
@@ -38,7 +41,8 @@
  *    zeroes it and reads it when convenient.
  *
  * Limits: 1 <= E <= 256, 1 <= k <= min(E, 8), T >= 0, T*k < 2^31, E*capacity < 2^31 (PADDED).
- * bf16 path: d and F multiples of 128. fp32 path: d a multiple of 4.
+ * bf16 path: d and F multiples of 128. fp32 path: d a multiple of 4. The free
+ * products and moe_dropout have limits of their own.
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
@@ -68,6 +72,8 @@ extern "C" {
 #define MOE_STATUS_NAN_LOGIT 1  /* a router logit was NaN (treated as -inf) */
 #define MOE_STATUS_BAD_ROUTE 2  /* an index out of [0,E) or repeated within a token (slot dropped) */
 #define MOE_STATUS_TIMEOUT   4  /* a bounded on-chip wait gave up (output invalid) */
+#define MOE_STATUS_BAD_OFFSETS 32 /* group offsets that fall or leave [0, rows] (clamped; those groups' outputs are
+                                     invalid, nothing outside the buffers is touched) */
 /* MXFP8 precision only, informational (the output is valid): */
 #define MOE_STATUS_MX_SATURATED 8   /* an element was clamped to +-448 when quantised; the OCP scale
                                        rule does this whenever a block's largest magnitude has a
@@ -175,6 +181,15 @@ extern "C" {
 #define MOE_PREACT_RECOMPUTE 0
 #define MOE_PREACT_SAVE      1
 
+/* Activations of the free products (moe_grouped_gemm, moe_linear): the
+ * identity, max(z, 0), z Phi(z) (Phi the normal distribution function),
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2, and z / (1 + e^-z). */
+#define MOE_ACT_NONE      0
+#define MOE_ACT_RELU      1
+#define MOE_ACT_GELU      2
+#define MOE_ACT_GELU_TANH 3
+#define MOE_ACT_SILU      4
+
 #define MOE_OP_ROUTE       0
 #define MOE_OP_PERMUTE     1
 #define MOE_OP_GROUPED_FFN 2
@@ -201,6 +216,25 @@ typedef struct moe_config {
   int32_t combine;      /* MOE_COMBINE_*: separate combine kernel or fused into the down projection (layer only) */
   int32_t preact;       /* MOE_PREACT_*: gate/up pre-activations recomputed or kept for the backward (layer only) */
 } moe_config;
+
+/* A free product's shapes. The row strides are in elements; 0 stands for
+ * contiguous rows. bf16 strides are multiples of 8 (rows start on 16 bytes;
+ * the widths n and k may be odd inside them), fp32 strides are free. A stride
+ * is at least the width of its rows. */
+typedef struct moe_gemm_config {
+  int32_t rows;     /* rows of x, y, dy, dx, residual, z and preact, all groups together */
+  int32_t n;        /* output features: columns of y and dy, rows of each W */
+  int32_t k;        /* input features: columns of x and dx, columns of each W */
+  int32_t groups;   /* experts E (the dense entry points: 1) */
+  int32_t dtype;    /* MOE_DTYPE_*: x, w, y, dy, dx, residual, z, preact; bias, dw, dbias are fp32 */
+  int32_t act;      /* MOE_ACT_* */
+  int64_t ldx;      /* row stride of x and dx (0: k) */
+  int64_t ldw;      /* row stride of W (0: k) */
+  int64_t w_stride; /* from one group's W to the next (0: n * ldw) */
+  int64_t ldy;      /* row stride of y and dy (0: n) */
+  int64_t ldr;      /* row stride of residual (0: the width of the output it is added to) */
+  int64_t ldz;      /* row stride of preact (0: n) and z (0: k; moe_act_backward: n) */
+} moe_gemm_config;
 
 typedef void* moe_stream_t; /* cudaStream_t */
 
@@ -396,6 +430,93 @@ MOE_API int32_t moe_pack_weights_mxfp8(const moe_config* cfg, const void* w13_pa
  * and MOE_STATUS_TIMEOUT is OR-ed into the status word; that call's outputs
  * are invalid and the context stays usable. n = 0 cancels. */
 MOE_API int32_t moe_debug_stall_next_gemms(int32_t n);
+
+/* moe_grouped_gemm -- one matrix product per expert over ragged row groups,
+ * with bias, activation and residual in its epilogue:
+ *   u[r, j] = sum_i x[r, i] w[e, j, i] + bias[e, j]     r in [offsets[e], offsets[e+1])
+ *   y[r, j] = act(u[r, j]) + residual[r, j]
+ * for experts other than moe_grouped_ffn's SwiGLU (one projection, any
+ * activation, biases), over the row groups that moe_permute writes.
+ * x [rows, k], w [groups, n, k], bias [groups, n] fp32 or NULL, residual
+ * [rows, n] or NULL (may be y itself: same address and stride), preact
+ * [rows, n] or NULL: receives u for the backward. offsets [groups + 1] int32
+ * on the device. Groups may be empty; rows outside every group are left as
+ * they were. Sums, bias, activation and residual are fp32, rounded once each
+ * to y and preact. fp32 products run on the CUDA cores in IEEE fp32, bf16
+ * ones on tensor cores. No workspace. Deterministic.
+ * Limits: 1 <= groups <= MOE_MAX_E, n, k >= 1, n * groups < 2^31.
+ * Errors: MOE_ERR_INVALID_ARG (NULL, negative sizes, a stride below its
+ * width, unknown act or dtype), MOE_ERR_UNSUPPORTED (limits, a pointer off 16
+ * bytes, a bf16 stride that is no multiple of 8). rows == 0 is MOE_OK. */
+MOE_API int32_t moe_grouped_gemm(const moe_gemm_config* cfg, const void* x, const int32_t* offsets, const void* w,
+                                 const float* bias, const void* residual, void* preact, void* y, int32_t* status_dev,
+                                 moe_stream_t stream);
+
+/* moe_grouped_gemm_dgrad -- the input gradient, through the activation that
+ * produced the input, in one kernel:
+ *   dx[r, i] = act'(z[r, i]) sum_j dy[r, j] w[e, j, i] + residual[r, i]
+ * dy [rows, n] is the gradient of u (the product's pre-activation; with
+ * MOE_ACT_NONE, of y). z [rows, k] or NULL: the pre-activations that x came
+ * from (x = act(z), as the previous moe_grouped_gemm's preact holds them),
+ * whose slope turns the gradient of x into that of z. residual [rows, k] or
+ * NULL: another path's gradient added to it. w is read as moe_grouped_gemm
+ * reads it, with no transposed copy. Rows outside every group are left alone. */
+MOE_API int32_t moe_grouped_gemm_dgrad(const moe_gemm_config* cfg, const void* dy, const int32_t* offsets,
+                                       const void* w, const void* z, const void* residual, void* dx,
+                                       int32_t* status_dev, moe_stream_t stream);
+
+/* moe_grouped_gemm_wgrad -- the weight and bias gradients (fp32, written, not
+ * added to):
+ *   dw[e, j, i] = sum_r dy[r, j] x[r, i],  dbias[e, j] = sum_r dy[r, j]
+ * over group e's rows; zero for an empty group. dw [groups, n, k] contiguous
+ * or NULL, dbias [groups, n] or NULL. */
+MOE_API int32_t moe_grouped_gemm_wgrad(const moe_gemm_config* cfg, const void* dy, const int32_t* offsets,
+                                       const void* x, float* dw, float* dbias, int32_t* status_dev,
+                                       moe_stream_t stream);
+
+/* moe_linear, moe_linear_dgrad, moe_linear_wgrad -- the same three for one
+ * dense weight w [n, k] over all rows (cfg->groups == 1): a shared expert or
+ * a dense layer beside the routed ones, whose residual is the routed output. */
+MOE_API int32_t moe_linear(const moe_gemm_config* cfg, const void* x, const void* w, const float* bias,
+                           const void* residual, void* preact, void* y, int32_t* status_dev, moe_stream_t stream);
+MOE_API int32_t moe_linear_dgrad(const moe_gemm_config* cfg, const void* dy, const void* w, const void* z,
+                                 const void* residual, void* dx, int32_t* status_dev, moe_stream_t stream);
+MOE_API int32_t moe_linear_wgrad(const moe_gemm_config* cfg, const void* dy, const void* x, float* dw, float* dbias,
+                                 int32_t* status_dev, moe_stream_t stream);
+
+/* moe_act_backward -- dz[r, j] = dy[r, j] act'(z[r, j]) over [rows, n], for an
+ * activation whose output no further product consumes (else
+ * moe_*_dgrad applies it). dy: stride ldy, z: ldz, dz: ldr (0: n). dz may be dy. */
+MOE_API int32_t moe_act_backward(const moe_gemm_config* cfg, const void* dy, const void* z, void* dz,
+                                 moe_stream_t stream);
+
+/* moe_dropout -- residual dropout with a mask that is never stored:
+ *   y[r, c] = residual[r, c] + (word(r, c) >= floor(p 2^32) ? x[r, c] / (1 - p) : 0)
+ * word(r, c) is word c % 4 of Philox4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) with the 128-bit counter
+ * (c / 4, r, o mod 2^32, o / 2^32), o = rng[1] + offset mod 2^64, under the
+ * key rng[0]. rng: two uint64 in DEVICE memory, so that a captured graph draws
+ * a new mask on every replay once the caller has moved rng[1]; calls that
+ * share rng tell their masks apart by `offset`. The mask depends on the
+ * element's place alone. A dropped element is zero whatever x holds there.
+ * The backward is the same call on dy without a residual: dx = moe_dropout(dy);
+ * the residual's gradient is dy.
+ * x, residual (or NULL), y: [rows, cols] of dtype with strides ldx, ldr, ldy
+ * in elements (0: cols). y may be x or the residual (same stride). Sums are
+ * fp32, rounded once. 0 <= p < 1; p == 0 reads no rng (it may be NULL). */
+MOE_API int32_t moe_dropout(int32_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ldx,
+                            const void* residual, int64_t ldr, void* y, int64_t ldy, double p, const uint64_t* rng,
+                            uint64_t offset, moe_stream_t stream);
+
+/* moe_unpermute_combine_dropout -- the end of a training block in one pass:
+ * moe_unpermute_combine's sum (fp32, not rounded in between), moe_dropout's
+ * mask on it (rows t, columns of d) and the residual stream added:
+ *   y[t] = residual[t] + dropout(sum_j topk_gate[t, j] y_perm[dest_row[t, j]])
+ * residual [T, d] (dtype) or NULL; it may be y. The gradient that enters
+ * moe_layer_backward is moe_dropout(dy) with the same p, rng and offset. */
+MOE_API int32_t moe_unpermute_combine_dropout(const moe_config* cfg, const void* y_perm, const int32_t* dest_row,
+                                              const float* topk_gate, const void* residual, double p,
+                                              const uint64_t* rng, uint64_t offset, void* y, moe_stream_t stream);
 
 /* moe_permute_static_scratch -- moe_permute for callers that cannot allocate.
  * The paper has no counterpart for this entry point. It is for code that has
