@@ -48,7 +48,7 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   if (c.ldy == 0) c.ldy = c.n;
   if (c.ldr == 0) c.ldr = u.r_width;
   if (c.ldz == 0) c.ldz = u.z_width;
-  if (c.w_stride == 0) c.w_stride = c.ldw * c.n;
+  if (c.w_stride == 0 || c.groups == 1) c.w_stride = c.ldw * c.n;
   const bool bf16 = c.dtype == MOE_DTYPE_BF16;
   p.rc = MOE_OK;
   if (u.x && !stride_ok(c.ldx, c.k, bf16, p.rc)) return p;
@@ -67,7 +67,7 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
 }
 
 cudaError_t launch_product(int dtype, MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
-  return dtype == MOE_DTYPE_F32 ? launch_matmul_f32(mode, a, s) : launch_matmul_bf16_simt(mode, a, s);
+  return dtype == MOE_DTYPE_F32 ? launch_matmul_f32(mode, a, s) : launch_matmul_tc(mode, a, s);
 }
 
 int forward(const moe_gemm_config* cfg, bool dense, const void* x, const int32_t* offsets, const void* w,

@@ -103,52 +103,82 @@ constexpr float kGeluTanhC = 0.7978845608028654f;  // sqrt(2 / pi)
 
 // The tanh form of GELU is z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3),
 // since (1 + tanh u) / 2 = sigmoid(2 u): no cancellation for negative z.
-template <bool kFast>
-MOE_DEV float act_of(float z, int act) {
+template <int kAct, bool kFast>
+MOE_DEV float act_value(float z) {
+  if constexpr (kAct == MOE_ACT_RELU) {
+    return z > 0.0f ? z : (z != z ? z : 0.0f);
+  } else if constexpr (kAct == MOE_ACT_GELU) {
+    float gauss;
+    // erfc keeps its relative precision in the negative tail
+    return z * (kFast ? phi_fast(z, gauss) : 0.5f * erfcf(-z * 0.70710678118654752f));
+  } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
+    return z * sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
+  } else if constexpr (kAct == MOE_ACT_SILU) {
+    return z * sigmoid_of<kFast>(z);
+  } else {
+    return z;
+  }
+}
+
+template <int kAct, bool kFast>
+MOE_DEV float slope_value(float z) {
+  if constexpr (kAct == MOE_ACT_RELU) {
+    return z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (kAct == MOE_ACT_GELU) {
+    float gauss, phi;
+    if constexpr (kFast) {
+      phi = phi_fast(z, gauss);
+    } else {
+      phi = 0.5f * erfcf(-z * 0.70710678118654752f);
+      gauss = expf(-0.5f * z * z);
+    }
+    return fmaf(z * 0.3989422804014327f, gauss, phi);
+  } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
+    const float s = sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
+    const float du = 2.0f * kGeluTanhC * (1.0f + 3.0f * 0.044715f * z * z);
+    return fmaf(z * s * (1.0f - s), du, s);
+  } else if constexpr (kAct == MOE_ACT_SILU) {
+    const float s = sigmoid_of<kFast>(z);
+    return s * fmaf(z, 1.0f - s, 1.0f);
+  } else {
+    return 1.0f;
+  }
+}
+
+// f(Act<kAct>) for the activation `act`: the branch is taken once around f.
+template <int kAct>
+struct Act {
+  static constexpr int value = kAct;
+};
+
+template <typename F>
+MOE_DEV void with_act(int act, F&& f) {
   switch (act) {
     case MOE_ACT_RELU:
-      return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case MOE_ACT_GELU: {
-      float gauss;
-      // erfc keeps its relative precision in the negative tail
-      return z * (kFast ? phi_fast(z, gauss) : 0.5f * erfcf(-z * 0.70710678118654752f));
-    }
+      return f(Act<MOE_ACT_RELU>{});
+    case MOE_ACT_GELU:
+      return f(Act<MOE_ACT_GELU>{});
     case MOE_ACT_GELU_TANH:
-      return z * sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
+      return f(Act<MOE_ACT_GELU_TANH>{});
     case MOE_ACT_SILU:
-      return z * sigmoid_of<kFast>(z);
+      return f(Act<MOE_ACT_SILU>{});
     default:
-      return z;
+      return f(Act<MOE_ACT_NONE>{});
   }
 }
 
 template <bool kFast>
+MOE_DEV float act_of(float z, int act) {
+  float v;
+  with_act(act, [&](auto k) { v = act_value<decltype(k)::value, kFast>(z); });
+  return v;
+}
+
+template <bool kFast>
 MOE_DEV float act_slope(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU:
-      return z > 0.0f ? 1.0f : 0.0f;
-    case MOE_ACT_GELU: {
-      float gauss, phi;
-      if (kFast) {
-        phi = phi_fast(z, gauss);
-      } else {
-        phi = 0.5f * erfcf(-z * 0.70710678118654752f);
-        gauss = expf(-0.5f * z * z);
-      }
-      return fmaf(z * 0.3989422804014327f, gauss, phi);
-    }
-    case MOE_ACT_GELU_TANH: {
-      const float s = sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
-      const float du = 2.0f * kGeluTanhC * (1.0f + 3.0f * 0.044715f * z * z);
-      return fmaf(z * s * (1.0f - s), du, s);
-    }
-    case MOE_ACT_SILU: {
-      const float s = sigmoid_of<kFast>(z);
-      return s * fmaf(z, 1.0f - s, 1.0f);
-    }
-    default:
-      return 1.0f;
-  }
+  float v;
+  with_act(act, [&](auto k) { v = slope_value<decltype(k)::value, kFast>(z); });
+  return v;
 }
 
 // ------------------------------------------------------------------ storage types
@@ -173,22 +203,21 @@ MOE_DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// One output element of rows mode from its sum: forward
+// One fp32 output element of rows mode from its sum: forward
 // act(sum + bias) + residual (the pre-activation stored first), input
-// gradient sum * act'(z) + residual; rounded once.
-template <typename T, bool kDgrad>
+// gradient sum * act'(z) + residual.
+template <bool kDgrad>
 MOE_DEV void finish_element(const MatmulArgs& a, float sum, int e, long long r, int n) {
-  constexpr bool kFast = sizeof(T) == 2;
   float v = sum;
   if constexpr (kDgrad) {
-    if (a.z != nullptr) v *= act_slope<kFast>(to_f32(static_cast<const T*>(a.z)[r * a.ldz + n]), a.act);
+    if (a.z != nullptr) v *= act_slope<false>(static_cast<const float*>(a.z)[r * a.ldz + n], a.act);
   } else {
     if (a.bias != nullptr) v += a.bias[static_cast<size_t>(e) * a.n + n];
-    if (a.preact != nullptr) static_cast<T*>(a.preact)[r * a.ldz + n] = from_f32<T>(v);
-    v = act_of<kFast>(v, a.act);
+    if (a.preact != nullptr) static_cast<float*>(a.preact)[r * a.ldz + n] = v;
+    v = act_of<false>(v, a.act);
   }
-  if (a.residual != nullptr) v += to_f32(static_cast<const T*>(a.residual)[r * a.ldr + n]);
-  static_cast<T*>(a.d)[r * a.ldd + n] = from_f32<T>(v);
+  if (a.residual != nullptr) v += static_cast<const float*>(a.residual)[r * a.ldr + n];
+  static_cast<float*>(a.d)[r * a.ldd + n] = v;
 }
 
 }  // namespace moe

@@ -49,14 +49,14 @@ MOE_DEV Quad load4(const T* p, int valid, bool vec) {
 
 // One operand's slice of BT (rows of the tile) x 16 (reduction), in registers.
 // kAlong: elements lie along the reduction (row-major tile rows); else across.
-template <typename T, bool kAlong, int BT>
+template <bool kAlong, int BT>
 struct Slice {
   static constexpr int kQuads = BT * kBK / 4 / kThreads;
   Quad q[kQuads];
 
   // base: element (first row of the tile, reduction index 0); rows and
   // depth: what of the tile and of the reduction [k0, ...) exists.
-  MOE_DEV void load(const T* base, long long ld, int rows, int k0, int depth, bool vec) {
+  MOE_DEV void load(const float* base, long long ld, int rows, int k0, int depth, bool vec) {
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
       const int id = threadIdx.x + i * kThreads;
@@ -109,7 +109,7 @@ MOE_DEV int at(int t, int i) {
   return BT == 128 ? (i >> 2) * 64 + t * 4 + (i & 3) : t * 4 + i;
 }
 
-template <typename T, MatmulMode kMode, int BT>
+template <MatmulMode kMode, int BT>
 __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs a) {
   constexpr int kPer = BT / 16;  // outputs of a thread along each axis
   constexpr bool kWeight = kMode == MatmulMode::kWgrad;
@@ -136,22 +136,22 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
     const long long rest = tile / tiles_n;
     int e, m0, m_valid, depth, k_first = 0;
     const int n0 = tn * BT, n_valid = min(BT, a.n - n0);
-    const T* pa;
-    const T* pb;
+    const float* pa;
+    const float* pb;
     if constexpr (kWeight) {
       e = static_cast<int>(rest / tiles_m);
       m0 = static_cast<int>(rest % tiles_m) * BT;
       m_valid = min(BT, a.m - m0);
       depth = s_rows[e].y - s_rows[e].x;
-      pa = static_cast<const T*>(a.a) + s_rows[e].x * a.lda + m0;
-      pb = static_cast<const T*>(a.b) + s_rows[e].x * a.ldb + n0;
+      pa = static_cast<const float*>(a.a) + s_rows[e].x * a.lda + m0;
+      pb = static_cast<const float*>(a.b) + s_rows[e].x * a.ldb + n0;
     } else {
       e = group_of_tile(prefix, a.groups, static_cast<int>(rest));
       m0 = s_rows[e].x + (static_cast<int>(rest) - prefix[e]) * BT;
       m_valid = min(BT, s_rows[e].y - m0);
       depth = a.k;
-      pa = static_cast<const T*>(a.a) + m0 * a.lda;
-      pb = static_cast<const T*>(a.b) + e * a.b_stride + (kMode == MatmulMode::kForward ? n0 * a.ldb : n0);
+      pa = static_cast<const float*>(a.a) + m0 * a.lda;
+      pb = static_cast<const float*>(a.b) + e * a.b_stride + (kMode == MatmulMode::kForward ? n0 * a.ldb : n0);
     }
     if (split > 1) {
       const int slices = (depth + kBK - 1) / kBK;
@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
 #pragma unroll
       for (int j = 0; j < kPer / 2; ++j) acc[i][j] = 0;
 
-    Slice<T, !kWeight, BT> qa;
-    Slice<T, kMode == MatmulMode::kForward, BT> qb;
+    Slice<!kWeight, BT> qa;
+    Slice<kMode == MatmulMode::kForward, BT> qb;
     if (k_first < depth) {
       qa.load(pa, a.lda, m_valid, k_first, depth, a.vec_a);
       qb.load(pb, a.ldb, n_valid, k_first, depth, a.vec_b);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
       if constexpr (kWeight)
         static_cast<float*>(a.d)[(static_cast<long long>(e) * a.m + m0 + i) * a.ldd + n0 + j] = v;
       else
-        finish_element<T, kMode == MatmulMode::kDgrad>(a, v, e, m0 + i, n0 + j);
+        finish_element<kMode == MatmulMode::kDgrad>(a, v, e, m0 + i, n0 + j);
     };
     if (BT == 64 && split > 1) {
       // partial tiles side by side in the cluster's shared memory, each CTA
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
   }
 }
 
-template <typename T, MatmulMode kMode>
+template <MatmulMode kMode>
 cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   const int sms = device_sm_count();
   // no more than these row tiles exist, however the rows fall to the groups
@@ -260,37 +260,28 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
     return tm * tn;
   };
   if (tiles(128) >= sms)
-    return launch_kernel(matmul_simt_kernel<T, kMode, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
+    return launch_kernel(matmul_simt_kernel<kMode, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
                          dim3(kThreads), 0, s, false, 1, a);
   const long long t = tiles(64);
   const int depth = kMode == MatmulMode::kWgrad ? a.rows : a.k;
   int split = 1;
   while (split < 8 && t * split * 2 <= 2 * sms && depth / (split * 2) >= 64) split *= 2;
   const long long grid = std::min<long long>(t, 4 * sms) * split;
-  return launch_kernel(matmul_simt_kernel<T, kMode, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, false,
+  return launch_kernel(matmul_simt_kernel<kMode, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, false,
                        static_cast<unsigned>(split), a);
 }
 
 }  // namespace
 
-template <typename T>
-cudaError_t launch_matmul_simt(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
   switch (mode) {
     case MatmulMode::kForward:
-      return launch_mode<T, MatmulMode::kForward>(a, s);
+      return launch_mode<MatmulMode::kForward>(a, s);
     case MatmulMode::kDgrad:
-      return launch_mode<T, MatmulMode::kDgrad>(a, s);
+      return launch_mode<MatmulMode::kDgrad>(a, s);
     default:
-      return launch_mode<T, MatmulMode::kWgrad>(a, s);
+      return launch_mode<MatmulMode::kWgrad>(a, s);
   }
-}
-
-cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
-  return launch_matmul_simt<float>(mode, a, s);
-}
-
-cudaError_t launch_matmul_bf16_simt(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
-  return launch_matmul_simt<__nv_bfloat16>(mode, a, s);
 }
 
 // ------------------------------------------------------------------ bias gradient

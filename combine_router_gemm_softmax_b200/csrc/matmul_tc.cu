@@ -1,0 +1,637 @@
+// The free products in bf16 (moe_grouped_gemm, moe_linear and their gradients)
+// on the tensor cores, over ragged row groups.
+//
+//   forward   D[r, j] = fin(sum_i x[r, i] W_e[j, i])      A = x, B = W_e
+//   dgrad     D[r, i] = fin(sum_j dy[r, j] W_e[j, i])     A = dy, B = W_e read across
+//   wgrad     D_e[j, i] = sum_r dy[r, j] x[r, i]          A = dy, B = x, both read across
+//
+// Nothing is transposed or packed beforehand: an operand whose reduction index
+// is the contiguous one enters the MMA K-major, one that lies across it
+// MN-major (both 128-byte swizzled tiles as the TMA loads write them, told
+// apart by the matrix and instruction descriptors). W is a three-dimensional
+// tensor map (k, n, group), so that what lies past a group's last row of W is
+// zero and not the next group's.
+//
+// Persistent CTAs (one an SM) walk a tile list built on the device from the
+// offsets. Warp 0 loads a ring of 4 stages (A 128 x 64, B 256 x 64: 48 KB),
+// one thread of warp 1 issues tcgen05.mma (128 x 256 x 16) into one of two TMEM
+// accumulators, warps 2..9 drain the other: bias, activation, slope and
+// residual in fp32, one rounding, and 32 x 32 blocks through shared memory to
+// TMA stores. The last column tile issues MMAs only as wide as it is (a
+// multiple of 16).
+//
+// wgrad's reduction is the group's rows: its last 64-row block may run into
+// the next group, so two more warps zero those rows of both operands in shared
+// memory (a row of a tile is 128 contiguous bytes whatever the swizzle) before
+// the MMA reads them. Zeroing one operand would not do: the other may hold NaN.
+//
+// When there are few tiles, a cluster of CTAs splits one tile's reduction
+// (kSplit): the partial tiles lie in the CTAs' own shared memory, and each CTA
+// adds its share of the 32 x 32 blocks over all of them in rank order, then
+// runs the epilogue on it. The same order on every run.
+#include "matmul_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBN = 256;
+constexpr int kBK = 64;
+constexpr int kStages = 4;
+constexpr int kEpiWarps = 8;
+constexpr uint32_t kABytes = kBM * kBK * 2;
+constexpr uint32_t kBBytes = kBN * kBK * 2;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kTmemCols = 2 * kBN;
+constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements
+
+struct TcArgs {
+  MatmulArgs p;
+  int n_tiles, m_tiles;  // column tiles; weight mode: row tiles of one group
+  int band;              // row tiles per band of the tile walk
+  int tma_store;         // D (and preact) have store maps
+};
+
+template <MatmulMode kMode>
+struct Shape {
+  static constexpr bool kWeight = kMode == MatmulMode::kWgrad;
+  static constexpr bool kAcrossA = kWeight;                       // A lies across the reduction
+  static constexpr bool kAcrossB = kMode != MatmulMode::kForward;  // B does
+  static constexpr int kThreads = kWeight ? 384 : 320;
+  static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 32 * 64;  // one 32 x 32 block of the output
+  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + kEpiWarps * kStgBytes +
+                                  (2 * kStages + 8) * 8 + 16 +
+                                  (kWeight ? 0 : kEpiWarps * 32 * 4 + kMaxE * 8 + (kMaxE + 1) * 4);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// Matrix descriptor of an MN-major tile: boxes of 64 reduction rows x 64
+// elements (128 bytes a row, 128-byte swizzle). Eight reduction rows are 1024
+// bytes; the next 64 elements along M or N are the next box. Sixteen reduction
+// rows further is 2048 bytes.
+MOE_DEV uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kBoxBytes >> 4) << 16;  // leading-dimension offset: 64 elements along M/N
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // stride: 8 rows along the reduction
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+template <bool kAcross>
+MOE_DEV uint64_t operand_desc(uint32_t tile, int kk) {
+  return kAcross ? sw128_mnmajor_desc(tile + kk * 2048) : sw128_kmajor_desc(tile + kk * 32);
+}
+
+// A tile: group, row tile, column tile, its blocks of 64 along the reduction,
+// and the group's rows.
+struct Tile {
+  int e, m, n, kb0, kb1;
+  int2 rows;
+};
+
+// 32 bf16 of a row from column n0 (n columns in all); columns past n are zero.
+MOE_DEV void load_row(const void* base, long long at, int n0, int n, float (&f)[32]) {
+  const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + at;
+  if (n0 + 32 <= n) {
+    uint4 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 t = __bfloat1622float2(h[j]);
+        f[8 * i + 2 * j] = t.x;
+        f[8 * i + 2 * j + 1] = t.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = n0 + i < n ? __bfloat162float(p[i]) : 0.0f;
+  }
+}
+
+// A lane's row of 32 columns to a bf16 matrix: the whole warp's block by TMA
+// where all 32 rows are the group's (`staged`), else row by row.
+MOE_DEV void store_rows(const float (&f)[32], void* base, long long at, int n0, int n, bool valid, bool staged,
+                        uint8_t* stg, int lane, const CUtensorMap* tm, int row0) {
+  uint32_t q[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) q[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  const uint4 v[4] = {make_uint4(q[0], q[1], q[2], q[3]), make_uint4(q[4], q[5], q[6], q[7]),
+                      make_uint4(q[8], q[9], q[10], q[11]), make_uint4(q[12], q[13], q[14], q[15])};
+  if (staged) {
+    stage_store_rows<64>(stg, v, lane, tm, n0, row0);
+  } else if (valid) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at;
+    if (n0 + 32 <= n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n0 + i < n) p[i] = __float2bfloat16_rn(f[i]);
+    }
+  }
+}
+
+// The epilogue of one 32 x 32 block of rows mode: this lane's row r (valid or
+// not), columns n0 .. n0 + 31, sums in f.
+template <bool kDgrad>
+MOE_DEV void finish_rows(const TcArgs& a, float (&f)[32], int e, long long r, int row0, int n0, bool valid, bool staged,
+                         uint8_t* stg, float* s_bias, int lane, const CUtensorMap* tm_d, const CUtensorMap* tm_p) {
+  const MatmulArgs& p = a.p;
+  float g[32];
+  if constexpr (kDgrad) {
+    if (p.z != nullptr && valid) {
+      load_row(p.z, r * p.ldz + n0, n0, p.n, g);
+      with_act(p.act, [&](auto k) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] *= slope_value<decltype(k)::value, true>(g[i]);
+      });
+    }
+  } else {
+    if (p.bias != nullptr) {
+      __syncwarp();
+      s_bias[lane] = n0 + lane < p.n ? p.bias[static_cast<size_t>(e) * p.n + n0 + lane] : 0.0f;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = *reinterpret_cast<const float4*>(s_bias + 4 * i);
+        f[4 * i] += b.x, f[4 * i + 1] += b.y, f[4 * i + 2] += b.z, f[4 * i + 3] += b.w;
+      }
+    }
+    if (p.preact != nullptr) store_rows(f, p.preact, r * p.ldz + n0, n0, p.n, valid, staged, stg, lane, tm_p, row0);
+    if (p.act != MOE_ACT_NONE)
+      with_act(p.act, [&](auto k) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = act_value<decltype(k)::value, true>(f[i]);
+      });
+  }
+  if (p.residual != nullptr && valid) {
+    load_row(p.residual, r * p.ldr + n0, n0, p.n, g);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] += g[i];
+  }
+  store_rows(f, p.d, r * p.ldd + n0, n0, p.n, valid, staged, stg, lane, tm_d, row0);
+}
+
+// The same for wgrad: row m of group e's fp32 gradient.
+MOE_DEV void finish_weight(const TcArgs& a, const float (&f)[32], int e, int m, int row0, int n0, uint8_t* stg, int lane,
+                           const CUtensorMap* tm_d) {
+  const MatmulArgs& p = a.p;
+  if (a.tma_store) {  // the map ends at the gradient's last row and column
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+          make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(tm_d, stg, n0, row0, e);
+      bulk_commit();
+    }
+  } else if (m < p.m) {
+    float* d = static_cast<float*>(p.d) + (static_cast<long long>(e) * p.m + m) * p.ldd + n0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n0 + i < p.n) d[i] = f[i];
+  }
+}
+
+template <MatmulMode kMode, bool kSplit>
+__global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
+    matmul_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_p,
+                     const TcArgs a) {
+  using S = Shape<kMode>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1024(smem_raw);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kStages * kABytes;
+  uint8_t* stg_all = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * S::kStgBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* wanted = tempty + 2;  // weight mode: the MMA thread has a block whose last rows are to be zeroed
+  uint64_t* zeroed = wanted + 1;  // and they are
+  uint64_t* drain = zeroed + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);  // 16-byte aligned, and what follows it
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* consumed_slot = reinterpret_cast<int*>(tmem_slot + 2);
+  // rows modes only
+  float* s_bias = reinterpret_cast<float*>(tmem_slot + 4);
+  int2* s_rows = reinterpret_cast<int2*>(s_bias + kEpiWarps * 32);
+  int* prefix = reinterpret_cast<int*>(s_rows + kMaxE);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const MatmulArgs& p = a.p;
+  uint32_t split = 1, part = 0;
+  if constexpr (kSplit) {
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    part = cluster_ctarank();
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], kEpiWarps);
+    }
+    mbar_init(wanted, 1);
+    mbar_init(zeroed, 2);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *consumed_slot = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    if (a.tma_store) tma_prefetch_desc(&tm_d);
+  }
+  if (warp == 0) {
+    if constexpr (S::kWeight) {
+      bool bad = false;
+      for (int e = lane; e < p.groups; e += 32) group_rows(p.offsets, e, p.rows, &bad);
+      if (bad && blockIdx.x == 0) report_status(p.status, MOE_STATUS_BAD_OFFSETS);
+    } else {
+      build_groups(p.offsets, p.groups, p.rows, 7, s_rows, prefix, p.status, lane);
+    }
+  } else if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int m_total = S::kWeight ? p.groups * a.m_tiles : prefix[p.groups];
+  const long long total = static_cast<long long>(m_total) * a.n_tiles;
+  const long long first_tile = kSplit ? blockIdx.x / split : blockIdx.x;
+  const long long step = kSplit ? (1LL << 62) : gridDim.x;  // a split CTA has one tile (or none)
+
+  // Bands of row tiles, each swept over all column tiles, so that a wave of
+  // CTAs shares A and B in L2; in weight mode the bands stay inside a group.
+  auto tile_at = [&](long long t) {
+    Tile c;
+    if constexpr (S::kWeight) {
+      const int per = a.m_tiles * a.n_tiles;
+      c.e = static_cast<int>(t / per);
+      const int rem = static_cast<int>(t - static_cast<long long>(c.e) * per);
+      const int b = rem / (a.band * a.n_tiles), within = rem - b * a.band * a.n_tiles;
+      const int rows = min(a.band, a.m_tiles - b * a.band);
+      c.m = b * a.band + within % rows;
+      c.n = within / rows;
+      c.rows = group_rows(p.offsets, c.e, p.rows);
+      c.kb0 = 0;
+      c.kb1 = (c.rows.y - c.rows.x + kBK - 1) / kBK;
+    } else {
+      const long long band_tiles = static_cast<long long>(a.band) * a.n_tiles;
+      const int b = static_cast<int>(t / band_tiles), within = static_cast<int>(t - b * band_tiles);
+      const int rows = min(a.band, m_total - b * a.band);
+      const int gm = b * a.band + within % rows;
+      c.n = within / rows;
+      c.e = group_of_tile(prefix, p.groups, gm);
+      c.m = gm - prefix[c.e];
+      c.rows = s_rows[c.e];
+      c.kb0 = 0;
+      c.kb1 = (p.k + kBK - 1) / kBK;
+    }
+    if constexpr (kSplit) {
+      const int blocks = c.kb1;
+      c.kb0 = static_cast<int>(static_cast<long long>(blocks) * part / split);
+      c.kb1 = static_cast<int>(static_cast<long long>(blocks) * (part + 1) / split);
+    }
+    return c;
+  };
+  // Rows of the group that block kb of the reduction holds (weight mode).
+  auto rows_in = [&](const Tile& c, int kb) { return c.rows.y - c.rows.x - kb * kBK; };
+
+  int issued = 0;
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      bool stop = false;
+      for (long long t = first_tile; t < total && !stop; t += step) {
+        const Tile c = tile_at(t);
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          const int s = issued % kStages;
+          if (!mbar_wait(&empty[s], ((issued / kStages) & 1) ^ 1, abort_flag)) {
+            *abort_flag = 1;
+            stop = true;
+            break;
+          }
+          mbar_expect_tx(&full[s], kStageBytes);
+          uint8_t* da = sA + s * kABytes;
+          uint8_t* db = sB + s * kBBytes;
+          if constexpr (S::kWeight) {
+            const int r = c.rows.x + kb * kBK;
+#pragma unroll
+            for (int i = 0; i < kBM / 64; ++i)
+              tma_load_2d(da + i * kBoxBytes, &tm_a, &full[s], c.m * kBM + i * 64, r);
+#pragma unroll
+            for (int i = 0; i < kBN / 64; ++i)
+              tma_load_2d(db + i * kBoxBytes, &tm_b, &full[s], c.n * kBN + i * 64, r);
+          } else {
+            tma_load_2d(da, &tm_a, &full[s], kb * kBK, c.rows.x + c.m * kBM);
+            if constexpr (S::kAcrossB) {
+#pragma unroll
+              for (int i = 0; i < kBN / 64; ++i)
+                tma_load_3d(db + i * kBoxBytes, &tm_b, &full[s], c.n * kBN + i * 64, kb * kBK, c.e);
+            } else {
+              tma_load_3d(db, &tm_b, &full[s], kb * kBK, c.n * kBN, c.e);
+            }
+          }
+          ++issued;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      int consumed = 0, local = 0;
+      uint32_t tails = 0;  // blocks that had rows zeroed
+      bool stop = false;
+      for (long long t = first_tile; t < total && !stop; t += step, ++local) {
+        const Tile c = tile_at(t);
+        const int acc = local & 1;
+        if (!mbar_wait(&tempty[acc], ((local >> 1) & 1) ^ 1, abort_flag)) {
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + acc * kBN;
+        const int width = min(kBN, (p.n - c.n * kBN + 15) & ~15);
+        const uint32_t idesc = idesc_bf16_f32(kBM, width) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          const int s = consumed % kStages;
+          bool ok = mbar_wait(&full[s], (consumed / kStages) & 1, abort_flag);
+          if constexpr (S::kWeight) {
+            if (ok && rows_in(c, kb) < kBK) {
+              mbar_arrive(wanted);
+              ok = mbar_wait(zeroed, tails++ & 1, abort_flag);
+            }
+          }
+          if (!ok) {
+            *abort_flag = 1;
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ta = smem_addr(sA + s * kABytes), tb = smem_addr(sB + s * kBBytes);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            umma_bf16(d_tmem, operand_desc<S::kAcrossA>(ta, kk), operand_desc<S::kAcrossB>(tb, kk), idesc,
+                      (kb != c.kb0) || (kk != 0));
+          umma_commit(&empty[s]);
+          ++consumed;
+        }
+        if (!stop) umma_commit(&tfull[acc]);
+      }
+      *consumed_slot = consumed;
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr);
+    }
+  } else if (S::kWeight && warp >= 2 + kEpiWarps) {
+    // ---------------------------------------------------------------- rows past the group (weight mode)
+    // One request at a time: the MMA thread waits for each answer.
+    int seen = 0;
+    uint32_t tails = 0;
+    for (long long t = first_tile; t < total; t += step) {
+      const Tile c = tile_at(t);
+      seen += c.kb1 - c.kb0;  // the tile's last block is the ring's block seen - 1
+      const int have = rows_in(c, c.kb1 - 1);
+      if (c.kb1 == c.kb0 || have >= kBK) continue;
+      if (!mbar_wait(wanted, tails++ & 1, abort_flag)) {
+        *abort_flag = 1;
+        break;
+      }
+      const int s = (seen - 1) % kStages;
+      const int chunks = (kBK - have) * 8;  // 16-byte chunks of one box
+      for (int i = threadIdx.x - 32 * (2 + kEpiWarps); i < chunks * ((kBM + kBN) / 64); i += 64) {
+        const int box = i / chunks, off = have * 128 + (i - box * chunks) * 16;
+        uint8_t* base =
+            box < kBM / 64 ? sA + s * kABytes + box * kBoxBytes : sB + s * kBBytes + (box - kBM / 64) * kBoxBytes;
+        *reinterpret_cast<uint4*>(base + off) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(zeroed);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;            // TMEM lane quadrant this warp may read
+    const int half = (warp - 2) >> 2;  // which half of the tile's columns it drains
+    uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
+    float* my_bias = s_bias + (warp - 2) * 32;
+    int local = 0;
+    for (long long t = first_tile; t < total; t += step, ++local) {
+      const Tile c = tile_at(t);
+      const int acc = local & 1;
+      if (!mbar_wait(&tfull[acc], (local >> 1) & 1, abort_flag)) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tbase = tmem + acc * kBN + (static_cast<uint32_t>(q * 32) << 16);
+      const bool none = c.kb1 == c.kb0;  // nothing was added: the accumulator was never written
+      if constexpr (kSplit) {
+        // the partial tile into the operand ring, which nothing reads any
+        // more: block (q, c32) of 32 rows x 128 bytes, 16-byte chunks swizzled
+#pragma unroll 1
+        for (int c32 = half * (kBN / 64); c32 < (half + 1) * (kBN / 64); ++c32) {
+          uint32_t v[32];
+          tmem_ld32(tbase + c32 * 32, v);
+          tmem_ld_wait();
+          uint8_t* row = smem + (c32 * 4 + q) * 4096 + lane * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) =
+                none ? make_uint4(0, 0, 0, 0) : make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      } else {
+        const int row0 = S::kWeight ? c.m * kBM + q * 32 : c.rows.x + c.m * kBM + q * 32;
+        const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;  // rows from row0 to the end
+#pragma unroll 1
+        for (int c0 = half * (kBN / 2); c0 < (half + 1) * (kBN / 2); c0 += 32) {
+          const int n0 = c.n * kBN + c0;
+          if (n0 >= p.n || left <= 0) break;
+          uint32_t v[32];
+          float f[32];
+          if (!none) {
+            tmem_ld32(tbase + c0, v);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = none ? 0.0f : __uint_as_float(v[i]);
+          if constexpr (S::kWeight)
+            finish_weight(a, f, c.e, row0 + lane, row0, n0, stg, lane, &tm_d);
+          else
+            finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left,
+                                                     a.tma_store && left >= 32, stg, my_bias, lane, &tm_d, &tm_p);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
+    }
+  }
+  __syncwarp();
+  if constexpr (kSplit) {
+    cluster_sync();  // every partial tile is in place
+    if (warp >= 2 && warp < 2 + kEpiWarps && first_tile < total && !*abort_flag) {
+      const Tile c = tile_at(first_tile);
+      uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
+      float* my_bias = s_bias + (warp - 2) * 32;
+      // 32 blocks of 32 x 32 shared out over the cluster's epilogue warps
+#pragma unroll 1
+      for (int b = part * kEpiWarps + warp - 2; b < (kBN / 32) * 4; b += split * kEpiWarps) {
+        const int q = b & 3, c32 = b >> 2;
+        const int n0 = c.n * kBN + c32 * 32;
+        const int row0 = S::kWeight ? c.m * kBM + q * 32 : c.rows.x + c.m * kBM + q * 32;
+        const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;
+        if (n0 >= p.n || left <= 0) continue;
+        const uint32_t row = smem_addr(smem) + b * 4096 + lane * 128;
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+#pragma unroll 1
+        for (uint32_t k = 0; k < split; ++k) {
+          const uint32_t peer = mapa_shared(row, k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float g[4];
+            ld_shared_cluster_v4(peer + ((j ^ (lane & 7)) << 4), g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[4 * j + i] += g[i];
+          }
+        }
+        if constexpr (S::kWeight)
+          finish_weight(a, f, c.e, row0 + lane, row0, n0, stg, lane, &tm_d);
+        else
+          finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left,
+                                                   a.tma_store && left >= 32, stg, my_bias, lane, &tm_d, &tm_p);
+      }
+    }
+    cluster_sync();  // nobody leaves while a peer reads its shared memory
+  }
+  if (warp >= 2 && lane == 0) bulk_wait_all();  // the staged stores have completed
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) report_status(p.status, MOE_STATUS_TIMEOUT);
+    if (warp == 0 && lane == 0) {
+      // loads issued but never consumed must land before the CTA leaves
+      for (int i = *consumed_slot; i < issued; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr);
+    }
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// A tensor map of up to three dimensions (contiguous first), strides in
+// elements. Host side; false if the driver refuses it.
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* base, int rank, const uint64_t* dims,
+            const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], one[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i] * bytes;
+  return encode_fn()(m, type, rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool load_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t groups,
+              uint64_t stride, uint32_t box_rows) {
+  const uint64_t dims[3] = {cols, rows, groups}, st[2] = {ld, stride};
+  const uint32_t box[3] = {64, box_rows, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, groups ? 3 : 2, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+bool store_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld) {
+  const uint64_t dims[2] = {cols, rows}, st[1] = {ld};
+  const uint32_t box[2] = {32, 32};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, 2, dims, st, box, CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+template <MatmulMode kMode, bool kSplit>
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const CUtensorMap& tp,
+                         const TcArgs& t, unsigned grid, unsigned split, cudaStream_t s) {
+  using S = Shape<kMode>;
+  auto* kernel = matmul_tc_kernel<kMode, kSplit>;
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+  if (err != cudaSuccess) return err;
+  return launch_kernel(kernel, dim3(grid), dim3(S::kThreads), S::kSmem, s, false, split, ta, tb, td, tp, t);
+}
+
+template <MatmulMode kMode>
+cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
+  using S = Shape<kMode>;
+  if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  CUtensorMap ta, tb, td{}, tp{};
+  TcArgs t{};
+  t.p = a;
+  t.n_tiles = (a.n + kBN - 1) / kBN;
+  bool ok;
+  if constexpr (S::kWeight) {
+    t.m_tiles = (a.m + kBM - 1) / kBM;
+    t.band = 16;
+    ok = load_map(&ta, a.a, a.m, a.rows, a.lda, 0, 0, 64) && load_map(&tb, a.b, a.n, a.rows, a.ldb, 0, 0, 64);
+    t.tma_store = a.ldd % 4 == 0;
+    if (t.tma_store) {
+      const uint64_t dims[3] = {static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.m), static_cast<uint64_t>(a.groups)};
+      const uint64_t st[2] = {static_cast<uint64_t>(a.ldd), static_cast<uint64_t>(a.ldd) * a.m};
+      const uint32_t box[3] = {32, 32, 1};
+      ok = ok && encode(&td, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.d, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    }
+  } else {
+    // a band of row tiles holds about 64 MB of A, so that it stays in L2 while the weights stream past it
+    const long long tile_bytes = 2LL * kBM * a.k;
+    t.band = 8;
+    while (t.band < 32 && t.band * 2 * tile_bytes <= (64LL << 20)) t.band *= 2;
+    constexpr bool fwd = kMode == MatmulMode::kForward;
+    ok = load_map(&ta, a.a, a.k, a.rows, a.lda, 0, 0, kBM) &&
+         load_map(&tb, a.b, fwd ? a.k : a.n, fwd ? a.n : a.k, a.ldb, a.groups, a.b_stride, fwd ? kBN : 64) &&
+         store_map(&td, a.d, a.n, a.rows, a.ldd) && (!a.preact || store_map(&tp, a.preact, a.n, a.rows, a.ldz));
+    t.tma_store = 1;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  // an upper bound of the row tiles, however the rows fall to the groups
+  const long long m_tiles = S::kWeight ? static_cast<long long>(a.groups) * t.m_tiles : (a.rows + kBM - 1LL) / kBM + a.groups - 1;
+  const long long tiles = m_tiles * t.n_tiles;
+  const int sms = device_sm_count();
+  const int blocks = ((S::kWeight ? a.rows / a.groups : a.k) + kBK - 1) / kBK;
+  unsigned split = 1;
+  while (split < 8 && tiles * split * 2 <= sms && blocks >= static_cast<int>(split) * 4) split *= 2;
+  if (split > 1) return launch_tiles<kMode, true>(ta, tb, td, tp, t, static_cast<unsigned>(tiles * split), split, s);
+  return launch_tiles<kMode, false>(ta, tb, td, tp, t, static_cast<unsigned>(std::min<long long>(tiles, sms)), 1, s);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+  switch (mode) {
+    case MatmulMode::kForward:
+      return launch_mode<MatmulMode::kForward>(a, s);
+    case MatmulMode::kDgrad:
+      return launch_mode<MatmulMode::kDgrad>(a, s);
+    default:
+      return launch_mode<MatmulMode::kWgrad>(a, s);
+  }
+}
+
+}  // namespace moe

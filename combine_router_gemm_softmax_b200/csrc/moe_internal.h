@@ -197,7 +197,9 @@ struct MatmulArgs {
 };
 // matmul_simt.cu
 cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
-cudaError_t launch_matmul_bf16_simt(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+// matmul_tc.cu (strides and addresses on 16 bytes)
+cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+// matmul_simt.cu
 cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const int32_t* offsets, int groups, int rows,
                                int n, float* out, bool vec, cudaStream_t s);
 cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const void* z, long long ldz, void* dz,
