@@ -21,9 +21,16 @@
 // multiple of 16).
 //
 // wgrad's reduction is the group's rows: its last 64-row block may run into
-// the next group, so two more warps zero those rows of both operands in shared
-// memory (a row of a tile is 128 contiguous bytes whatever the swizzle) before
-// the MMA reads them. Zeroing one operand would not do: the other may hold NaN.
+// the next group, so warp 1 zeroes those rows of both operands in shared memory
+// (a row of a tile is 128 contiguous bytes whatever the swizzle) before the MMA
+// reads them. Zeroing one operand would not do: the other may hold NaN.
+//
+// The tensor cores add into an fp32 accumulator by truncation, which biases a
+// long sum towards zero by about 1.1e-9 of it a row (measured: 1.9e-5 over
+// 16384 rows). bf16 outputs do not notice; wgrad's fp32 ones would. So wgrad
+// keeps an accumulator for kChainBlocks blocks (512 rows: 4.7e-7) only and the
+// epilogue adds these partial sums, rounded to nearest, in registers, while
+// the MMAs fill the other accumulator.
 //
 // When there are few tiles, a cluster of CTAs splits one tile's reduction
 // (kSplit): the partial tiles lie in the CTAs' own shared memory, and each CTA
@@ -39,6 +46,8 @@ constexpr int kBN = 256;
 constexpr int kBK = 64;
 constexpr int kStages = 4;
 constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kChainBlocks = 8;  // wgrad: blocks of the reduction added in one accumulator
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBBytes = kBN * kBK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
@@ -57,10 +66,9 @@ struct Shape {
   static constexpr bool kWeight = kMode == MatmulMode::kWgrad;
   static constexpr bool kAcrossA = kWeight;                       // A lies across the reduction
   static constexpr bool kAcrossB = kMode != MatmulMode::kForward;  // B does
-  static constexpr int kThreads = kWeight ? 384 : 320;
   static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 32 * 64;  // one 32 x 32 block of the output
   static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + kEpiWarps * kStgBytes +
-                                  (2 * kStages + 8) * 8 + 16 +
+                                  (2 * kStages + 6) * 8 + 16 +
                                   (kWeight ? 0 : kEpiWarps * 32 * 4 + kMaxE * 8 + (kMaxE + 1) * 4);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -205,7 +213,7 @@ MOE_DEV void finish_weight(const TcArgs& a, const float (&f)[32], int e, int m, 
 }
 
 template <MatmulMode kMode, bool kSplit>
-__global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_p,
                      const TcArgs a) {
@@ -219,9 +227,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* wanted = tempty + 2;  // weight mode: the MMA thread has a block whose last rows are to be zeroed
-  uint64_t* zeroed = wanted + 1;  // and they are
-  uint64_t* drain = zeroed + 1;
+  uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);  // 16-byte aligned, and what follows it
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* consumed_slot = reinterpret_cast<int*>(tmem_slot + 2);
@@ -247,8 +253,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], kEpiWarps);
     }
-    mbar_init(wanted, 1);
-    mbar_init(zeroed, 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *consumed_slot = 0;
@@ -312,8 +316,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     }
     return c;
   };
-  // Rows of the group that block kb of the reduction holds (weight mode).
-  auto rows_in = [&](const Tile& c, int kb) { return c.rows.y - c.rows.x - kb * kBK; };
 
   int issued = 0;
   if (warp == 0) {
@@ -355,76 +357,66 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer
-      int consumed = 0, local = 0;
-      uint32_t tails = 0;  // blocks that had rows zeroed
-      bool stop = false;
-      for (long long t = first_tile; t < total && !stop; t += step, ++local) {
-        const Tile c = tile_at(t);
-        const int acc = local & 1;
-        if (!mbar_wait(&tempty[acc], ((local >> 1) & 1) ^ 1, abort_flag)) {
-          *abort_flag = 1;
+    // ---------------------------------------------------------------- MMA issuer
+    // The whole warp walks the ring; lane 0 issues, and in weight mode all
+    // lanes zero the rows of a group's last block that belong to no one.
+    int consumed = 0, filled = 0;  // blocks taken from the ring, accumulators filled
+    bool stop = false;
+    for (long long t = first_tile; t < total && !stop; t += step) {
+      const Tile c = tile_at(t);
+      const int width = min(kBN, (p.n - c.n * kBN + 15) & ~15);
+      const uint32_t idesc = idesc_bf16_f32(kBM, width) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
+      for (int k0 = c.kb0; k0 < c.kb1 && !stop; k0 += S::kWeight ? kChainBlocks : c.kb1 - c.kb0, ++filled) {
+        const int acc = filled & 1;
+        if (!mbar_wait(&tempty[acc], ((filled >> 1) & 1) ^ 1, abort_flag)) {
+          stop = true;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem + acc * kBN;
-        const int width = min(kBN, (p.n - c.n * kBN + 15) & ~15);
-        const uint32_t idesc = idesc_bf16_f32(kBM, width) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        const int k1 = S::kWeight ? min(k0 + kChainBlocks, c.kb1) : c.kb1;
+        for (int kb = k0; kb < k1; ++kb) {
           const int s = consumed % kStages;
-          bool ok = mbar_wait(&full[s], (consumed / kStages) & 1, abort_flag);
-          if constexpr (S::kWeight) {
-            if (ok && rows_in(c, kb) < kBK) {
-              mbar_arrive(wanted);
-              ok = mbar_wait(zeroed, tails++ & 1, abort_flag);
-            }
-          }
-          if (!ok) {
-            *abort_flag = 1;
+          if (!mbar_wait(&full[s], (consumed / kStages) & 1, abort_flag)) {
             stop = true;
             break;
           }
-          tc_fence_after();
-          const uint32_t ta = smem_addr(sA + s * kABytes), tb = smem_addr(sB + s * kBBytes);
+          if constexpr (S::kWeight) {
+            const int have = c.rows.y - c.rows.x - kb * kBK;
+            if (have < kBK) {
+              const int chunks = (kBK - have) * 8;  // 16-byte chunks of one box
+#pragma unroll 1
+              for (int box = 0; box < (kBM + kBN) / 64; ++box) {
+                uint8_t* base =
+                    box < kBM / 64 ? sA + s * kABytes + box * kBoxBytes : sB + s * kBBytes + (box - kBM / 64) * kBoxBytes;
+                for (int i = lane; i < chunks; i += 32)
+                  *reinterpret_cast<uint4*>(base + have * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_shared();
+              __syncwarp();
+            }
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t ta = smem_addr(sA + s * kABytes), tb = smem_addr(sB + s * kBBytes);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            umma_bf16(d_tmem, operand_desc<S::kAcrossA>(ta, kk), operand_desc<S::kAcrossB>(tb, kk), idesc,
-                      (kb != c.kb0) || (kk != 0));
-          umma_commit(&empty[s]);
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              umma_bf16(d_tmem, operand_desc<S::kAcrossA>(ta, kk), operand_desc<S::kAcrossB>(tb, kk), idesc,
+                        (kb != k0) || (kk != 0));
+            umma_commit(&empty[s]);
+          }
+          __syncwarp();
           ++consumed;
         }
-        if (!stop) umma_commit(&tfull[acc]);
+        if (!stop && lane == 0) umma_commit(&tfull[acc]);
+        __syncwarp();
       }
+    }
+    if (lane == 0) {
+      if (stop) *abort_flag = 1;
       *consumed_slot = consumed;
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr);
-    }
-  } else if (S::kWeight && warp >= 2 + kEpiWarps) {
-    // ---------------------------------------------------------------- rows past the group (weight mode)
-    // One request at a time: the MMA thread waits for each answer.
-    int seen = 0;
-    uint32_t tails = 0;
-    for (long long t = first_tile; t < total; t += step) {
-      const Tile c = tile_at(t);
-      seen += c.kb1 - c.kb0;  // the tile's last block is the ring's block seen - 1
-      const int have = rows_in(c, c.kb1 - 1);
-      if (c.kb1 == c.kb0 || have >= kBK) continue;
-      if (!mbar_wait(wanted, tails++ & 1, abort_flag)) {
-        *abort_flag = 1;
-        break;
-      }
-      const int s = (seen - 1) % kStages;
-      const int chunks = (kBK - have) * 8;  // 16-byte chunks of one box
-      for (int i = threadIdx.x - 32 * (2 + kEpiWarps); i < chunks * ((kBM + kBN) / 64); i += 64) {
-        const int box = i / chunks, off = have * 128 + (i - box * chunks) * 16;
-        uint8_t* base =
-            box < kBM / 64 ? sA + s * kABytes + box * kBoxBytes : sB + s * kBBytes + (box - kBM / 64) * kBoxBytes;
-        *reinterpret_cast<uint4*>(base + off) = make_uint4(0, 0, 0, 0);
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(zeroed);
     }
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -432,56 +424,86 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     const int half = (warp - 2) >> 2;  // which half of the tile's columns it drains
     uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
     float* my_bias = s_bias + (warp - 2) * 32;
-    int local = 0;
-    for (long long t = first_tile; t < total; t += step, ++local) {
-      const Tile c = tile_at(t);
-      const int acc = local & 1;
-      if (!mbar_wait(&tfull[acc], (local >> 1) & 1, abort_flag)) {
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    int filled = 0;
+    auto wait_acc = [&]() {
+      if (!mbar_wait(&tfull[filled & 1], (filled >> 1) & 1, abort_flag)) {
         *abort_flag = 1;
-        break;
+        return false;
       }
       tc_fence_after();
-      const uint32_t tbase = tmem + acc * kBN + (static_cast<uint32_t>(q * 32) << 16);
-      const bool none = c.kb1 == c.kb0;  // nothing was added: the accumulator was never written
-      if constexpr (kSplit) {
-        // the partial tile into the operand ring, which nothing reads any
-        // more: block (q, c32) of 32 rows x 128 bytes, 16-byte chunks swizzled
-#pragma unroll 1
-        for (int c32 = half * (kBN / 64); c32 < (half + 1) * (kBN / 64); ++c32) {
-          uint32_t v[32];
-          tmem_ld32(tbase + c32 * 32, v);
-          tmem_ld_wait();
-          uint8_t* row = smem + (c32 * 4 + q) * 4096 + lane * 128;
+      return true;
+    };
+    auto free_acc = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[filled & 1]);
+      ++filled;
+    };
+    // a partial tile into the operand ring, which nothing reads any more:
+    // block (q, c32) of 32 rows x 128 bytes, 16-byte chunks swizzled
+    auto keep_partial = [&](int c32, const float (&f)[32]) {
+      uint8_t* row = smem + (c32 * 4 + q) * 4096 + lane * 128;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) =
-                none ? make_uint4(0, 0, 0, 0) : make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4)) =
+            make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+    };
+    for (long long t = first_tile; t < total; t += step) {
+      const Tile c = tile_at(t);
+      const int row0 = S::kWeight ? c.m * kBM + q * 32 : c.rows.x + c.m * kBM + q * 32;
+      const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;  // rows from row0 to the end
+      if constexpr (S::kWeight) {
+        float f[4][32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[b][i] = 0.0f;
+        bool ok = true;
+        for (int k0 = c.kb0; k0 < c.kb1; k0 += kChainBlocks) {
+          if (!(ok = wait_acc())) break;
+          const uint32_t tbase = tmem + (filled & 1) * kBN + lanes + half * (kBN / 2);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            uint32_t v[16];
+            tmem_ld16(tbase + b * 16, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[b >> 1][(b & 1) * 16 + i] += __uint_as_float(v[i]);
+          }
+          free_acc();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int c32 = half * 4 + b, n0 = c.n * kBN + c32 * 32;
+          if constexpr (kSplit) {
+            keep_partial(c32, f[b]);
+          } else {
+            if (n0 < p.n && left > 0) finish_weight(a, f[b], c.e, row0 + lane, row0, n0, stg, lane, &tm_d);
+          }
         }
       } else {
-        const int row0 = S::kWeight ? c.m * kBM + q * 32 : c.rows.x + c.m * kBM + q * 32;
-        const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;  // rows from row0 to the end
+        if (!wait_acc()) break;
+        const uint32_t tbase = tmem + (filled & 1) * kBN + lanes;
 #pragma unroll 1
         for (int c0 = half * (kBN / 2); c0 < (half + 1) * (kBN / 2); c0 += 32) {
           const int n0 = c.n * kBN + c0;
           if (n0 >= p.n || left <= 0) break;
           uint32_t v[32];
           float f[32];
-          if (!none) {
-            tmem_ld32(tbase + c0, v);
-            tmem_ld_wait();
-          }
+          tmem_ld32(tbase + c0, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = none ? 0.0f : __uint_as_float(v[i]);
-          if constexpr (S::kWeight)
-            finish_weight(a, f, c.e, row0 + lane, row0, n0, stg, lane, &tm_d);
+          for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+          if constexpr (kSplit)
+            keep_partial(c0 / 32, f);
           else
             finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left,
                                                      a.tma_store && left >= 32, stg, my_bias, lane, &tm_d, &tm_p);
         }
+        free_acc();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
     }
   }
   __syncwarp();
@@ -574,7 +596,7 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUt
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
-  return launch_kernel(kernel, dim3(grid), dim3(S::kThreads), S::kSmem, s, false, split, ta, tb, td, tp, t);
+  return launch_kernel(kernel, dim3(grid), dim3(kThreads), S::kSmem, s, false, split, ta, tb, td, tp, t);
 }
 
 template <MatmulMode kMode>
