@@ -13,12 +13,25 @@
 // zero and not the next group's.
 //
 // Persistent CTAs (one an SM) walk a tile list built on the device from the
-// offsets. Warp 0 loads a ring of 4 stages (A 128 x 64, B 256 x 64: 48 KB),
-// one thread of warp 1 issues tcgen05.mma (128 x 256 x 16) into one of two TMEM
-// accumulators, warps 2..9 drain the other: bias, activation, slope and
-// residual in fp32, one rounding, and 32 x 32 blocks through shared memory to
-// TMA stores. The last column tile issues MMAs only as wide as it is (a
-// multiple of 16).
+// offsets. Warp 0 loads a ring of up to 8 stages (192 KB) by TMA, one thread
+// of warp 1 issues tcgen05.mma into one of two TMEM accumulators, warps 2..9
+// drain the other: bias, activation, slope and residual in fp32, one rounding,
+// and 32 x 32 blocks through shared memory to TMA stores. Three forms:
+//
+//   kPair    256 x bn tiles on a cluster of two CTAs (cta_group::2): each loads
+//            128 rows of A and half of B, 32 KB a stage at bn = 256, so that
+//            six stages cover 3000 cycles of load latency. The form for large
+//            products.
+//   kSingle  128 x bn tiles, a CTA each (48 KB a stage): groups of few rows,
+//            whose 256-row tiles would be padding.
+//   kSplit   a cluster of CTAs shares one 128 x bn tile's reduction when there
+//            are few tiles: the partial tiles lie in the CTAs' own shared
+//            memory, and each CTA adds its share of the 32 x 32 blocks over all
+//            of them in rank order, then runs the epilogue on it (the same
+//            order on every run).
+//
+// The width bn is chosen per call so that the tiles fill the SMs evenly
+// (choose_tiles); the last column tile issues MMAs only as wide as it is.
 //
 // wgrad's reduction is the group's rows: its last 64-row block may run into
 // the next group, so warp 1 zeroes those rows of both operands in shared memory
@@ -31,35 +44,39 @@
 // keeps an accumulator for kChainBlocks blocks (512 rows: 4.7e-7) only and the
 // epilogue adds these partial sums, rounded to nearest, in registers, while
 // the MMAs fill the other accumulator.
-//
-// When there are few tiles, a cluster of CTAs splits one tile's reduction
-// (kSplit): the partial tiles lie in the CTAs' own shared memory, and each CTA
-// adds its share of the 32 x 32 blocks over all of them in rank order, then
-// runs the epilogue on it. The same order on every run.
+#include <cmath>
+
 #include "matmul_common.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kBM = 128;
-constexpr int kBN = 256;
+constexpr int kBN = 256;  // columns of an accumulator: the widest tile
 constexpr int kBK = 64;
-constexpr int kStages = 4;
+constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kChainBlocks = 8;  // wgrad: blocks of the reduction added in one accumulator
-constexpr uint32_t kABytes = kBM * kBK * 2;
-constexpr uint32_t kBBytes = kBN * kBK * 2;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kABytes = kBM * kBK * 2;  // one CTA's rows of A
+constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements
 
+enum class Form { kSingle, kSplit, kPair };
+
 struct TcArgs {
   MatmulArgs p;
+  int bn;                // columns of a tile: a multiple of 32 up to kBN
+  int stages;            // of the operand ring
+  uint32_t stage_bytes;  // of one CTA's ring
   int n_tiles, m_tiles;  // column tiles; weight mode: row tiles of one group
   int band;              // row tiles per band of the tile walk
   int tma_store;         // D (and preact) have store maps
 };
+
+// full, empty, tails and zeroed per stage, two accumulators' full and empty, the drain; even
+constexpr int kBarriers = 4 * kMaxStages + 6;
 
 template <MatmulMode kMode>
 struct Shape {
@@ -67,8 +84,7 @@ struct Shape {
   static constexpr bool kAcrossA = kWeight;                       // A lies across the reduction
   static constexpr bool kAcrossB = kMode != MatmulMode::kForward;  // B does
   static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 32 * 64;  // one 32 x 32 block of the output
-  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + kEpiWarps * kStgBytes +
-                                  (2 * kStages + 6) * 8 + 16 +
+  static constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStgBytes + kBarriers * 8 + 16 +
                                   (kWeight ? 0 : kEpiWarps * 32 * 4 + kMaxE * 8 + (kMaxE + 1) * 4);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -88,8 +104,8 @@ MOE_DEV uint64_t sw128_mnmajor_desc(uint32_t saddr) {
 }
 
 template <bool kAcross>
-MOE_DEV uint64_t operand_desc(uint32_t tile, int kk) {
-  return kAcross ? sw128_mnmajor_desc(tile + kk * 2048) : sw128_kmajor_desc(tile + kk * 32);
+MOE_DEV uint64_t operand_desc(uint32_t tile) {
+  return kAcross ? sw128_mnmajor_desc(tile) : sw128_kmajor_desc(tile);
 }
 
 // A tile: group, row tile, column tile, its blocks of 64 along the reduction,
@@ -98,6 +114,24 @@ struct Tile {
   int e, m, n, kb0, kb1;
   int2 rows;
 };
+
+// Tile loads completing on the barrier at `bar` (of this CTA, or with kPair of
+// the pair's CTA whose address it is).
+template <bool kPair>
+MOE_DEV void load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  if constexpr (kPair)
+    tma_load_2d_pair(dst, map, bar, x, y);
+  else
+    tma_load_2d_at(dst, map, bar, x, y);
+}
+
+template <bool kPair>
+MOE_DEV void load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  if constexpr (kPair)
+    tma_load_3d_pair(dst, map, bar, x, y, z);
+  else
+    tma_load_3d_at(dst, map, bar, x, y, z);
+}
 
 // 32 bf16 of a row from column n0 (n columns in all); columns past n are zero.
 MOE_DEV void load_row(const void* base, long long at, int n0, int n, float (&f)[32]) {
@@ -212,23 +246,38 @@ MOE_DEV void finish_weight(const TcArgs& a, const float (&f)[32], int e, int m, 
   }
 }
 
-template <MatmulMode kMode, bool kSplit>
+// One rows-mode or weight-mode block of 32 x 32 to its epilogue.
+template <MatmulMode kMode>
+MOE_DEV void finish_block(const TcArgs& a, float (&f)[32], const Tile& c, int row0, int left, int n0, uint8_t* stg,
+                          float* s_bias, int lane, const CUtensorMap* tm_d, const CUtensorMap* tm_p) {
+  if constexpr (Shape<kMode>::kWeight)
+    finish_weight(a, f, c.e, row0 + lane, row0, n0, stg, lane, tm_d);
+  else
+    finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left, a.tma_store && left >= 32,
+                                             stg, s_bias, lane, tm_d, tm_p);
+}
+
+template <MatmulMode kMode, Form kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_p,
                      const TcArgs a) {
   using S = Shape<kMode>;
+  constexpr bool kPair = kForm == Form::kPair, kSplit = kForm == Form::kSplit;
+  constexpr int kTileM = kPair ? 2 * kBM : kBM;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_1024(smem_raw);
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kABytes;
-  uint8_t* stg_all = smem + kStages * kStageBytes;
+  uint8_t* smem = align_1024(smem_raw);  // the ring: per stage A, then B
+  uint8_t* stg_all = smem + kRingBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * S::kStgBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  uint64_t* empty = full + kMaxStages;
+  // kPair, weight mode, a block with rows to zero: the second CTA's loads
+  // complete on its own tails[s], and its zeroing on the leader's zeroed[s]
+  uint64_t* tails = empty + kMaxStages;
+  uint64_t* zeroed = tails + kMaxStages;
+  uint64_t* tfull = zeroed + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);  // 16-byte aligned, and what follows it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + kBarriers);  // 16-byte aligned, and what follows it
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* consumed_slot = reinterpret_cast<int*>(tmem_slot + 2);
   // rows modes only
@@ -238,20 +287,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const MatmulArgs& p = a.p;
-  uint32_t split = 1, part = 0;
-  if constexpr (kSplit) {
+  uint32_t split = 1, rank = 0;  // CTAs of the cluster, this one's place
+  if constexpr (kForm != Form::kSingle) {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
-    part = cluster_ctarank();
+    rank = cluster_ctarank();
   }
+  const bool leader = rank == 0;
+  auto raise_abort = [&]() {
+    *abort_flag = 1;
+    if constexpr (kPair) st_shared_cluster_u32(mapa_shared(smem_addr(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
+  };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&tails[s], 1);
+      mbar_init(&zeroed[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kEpiWarps);
+      mbar_init(&tempty[i], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -267,20 +323,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = lane; e < p.groups; e += 32) group_rows(p.offsets, e, p.rows, &bad);
       if (bad && blockIdx.x == 0) report_status(p.status, MOE_STATUS_BAD_OFFSETS);
     } else {
-      build_groups(p.offsets, p.groups, p.rows, 7, s_rows, prefix, p.status, lane);
+      build_groups(p.offsets, p.groups, p.rows, kPair ? 8 : 7, s_rows, prefix, p.status, lane);
     }
   } else if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // both CTAs' barriers are initialised before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int m_total = S::kWeight ? p.groups * a.m_tiles : prefix[p.groups];
   const long long total = static_cast<long long>(m_total) * a.n_tiles;
-  const long long first_tile = kSplit ? blockIdx.x / split : blockIdx.x;
-  const long long step = kSplit ? (1LL << 62) : gridDim.x;  // a split CTA has one tile (or none)
+  const long long first_tile = blockIdx.x / split;
+  const long long step = kSplit ? (1LL << 62) : gridDim.x / split;  // a split cluster has one tile (or none)
 
   // Bands of row tiles, each swept over all column tiles, so that a wave of
   // CTAs shares A and B in L2; in weight mode the bands stay inside a group.
@@ -311,124 +373,199 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if constexpr (kSplit) {
       const int blocks = c.kb1;
-      c.kb0 = static_cast<int>(static_cast<long long>(blocks) * part / split);
-      c.kb1 = static_cast<int>(static_cast<long long>(blocks) * (part + 1) / split);
+      c.kb0 = static_cast<int>(static_cast<long long>(blocks) * rank / split);
+      c.kb1 = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / split);
     }
     return c;
   };
+  // Columns the MMAs of a tile compute; each CTA of a pair loads half of them,
+  // and both halves are multiples of 16.
+  auto width_of = [&](const Tile& c) {
+    constexpr int kUnit = kPair ? 32 : 16;
+    return min(a.bn, (p.n - c.n * a.bn + kUnit - 1) & ~(kUnit - 1));
+  };
+  // Rows of the group in block kb of the reduction (weight mode); under kBK the rest is zeroed.
+  auto rows_in = [&](const Tile& c, int kb) { return c.rows.y - c.rows.x - kb * kBK; };
+  const int b_cols = kPair ? a.bn / 2 : a.bn;  // columns of B in this CTA's ring
+  const int b_boxes = (b_cols + 63) / 64;       // of a B that lies across
 
   int issued = 0;
+  uint32_t tail_seen = 0, tail_last = 0;  // kPair's second CTA: stages whose tails[] was used, and the last phase's parity
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      bool stop = false;
-      for (long long t = first_tile; t < total && !stop; t += step) {
-        const Tile c = tile_at(t);
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          const int s = issued % kStages;
-          if (!mbar_wait(&empty[s], ((issued / kStages) & 1) ^ 1, abort_flag)) {
-            *abort_flag = 1;
-            stop = true;
-            break;
-          }
-          mbar_expect_tx(&full[s], kStageBytes);
-          uint8_t* da = sA + s * kABytes;
-          uint8_t* db = sB + s * kBBytes;
+    int s = 0;
+    uint32_t phase = 0, tail_next = 0;
+    bool stop = false;
+    const uint32_t full_leader = kPair ? mapa_shared(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
+    for (long long t = first_tile; t < total && !stop; t += step) {
+      const Tile c = tile_at(t);
+      const int n0 = c.n * a.bn + (kPair ? static_cast<int>(rank) * (width_of(c) / 2) : 0);
+      const int m0 = c.m * kTileM + (kPair ? static_cast<int>(rank) * kBM : 0);
+      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        if (!mbar_wait(&empty[s], phase ^ 1, abort_flag)) {
+          raise_abort();
+          stop = true;
+          break;
+        }
+        const bool tail = kPair && S::kWeight && rows_in(c, kb) < kBK;
+        const bool own_tail = tail && !leader;
+        if (elect_one()) {
+          uint8_t* da = smem + s * a.stage_bytes;
+          uint8_t* db = da + kABytes;
+          const uint32_t bar = own_tail ? smem_addr(&tails[s]) : full_leader + s * 8;
+          if (own_tail)
+            mbar_expect_tx(&tails[s], a.stage_bytes);
+          else if (leader || !kPair)
+            mbar_expect_tx(&full[s], kPair && !tail ? 2 * a.stage_bytes : a.stage_bytes);
           if constexpr (S::kWeight) {
             const int r = c.rows.x + kb * kBK;
 #pragma unroll
-            for (int i = 0; i < kBM / 64; ++i)
-              tma_load_2d(da + i * kBoxBytes, &tm_a, &full[s], c.m * kBM + i * 64, r);
-#pragma unroll
-            for (int i = 0; i < kBN / 64; ++i)
-              tma_load_2d(db + i * kBoxBytes, &tm_b, &full[s], c.n * kBN + i * 64, r);
+            for (int i = 0; i < kBM / 64; ++i) load_2d<kPair>(da + i * kBoxBytes, &tm_a, bar, m0 + i * 64, r);
+            for (int i = 0; i < b_boxes; ++i) load_2d<kPair>(db + i * kBoxBytes, &tm_b, bar, n0 + i * 64, r);
           } else {
-            tma_load_2d(da, &tm_a, &full[s], kb * kBK, c.rows.x + c.m * kBM);
+            load_2d<kPair>(da, &tm_a, bar, kb * kBK, c.rows.x + m0);
             if constexpr (S::kAcrossB) {
-#pragma unroll
-              for (int i = 0; i < kBN / 64; ++i)
-                tma_load_3d(db + i * kBoxBytes, &tm_b, &full[s], c.n * kBN + i * 64, kb * kBK, c.e);
+              for (int i = 0; i < b_boxes; ++i) load_3d<kPair>(db + i * kBoxBytes, &tm_b, bar, n0 + i * 64, kb * kBK, c.e);
             } else {
-              tma_load_3d(db, &tm_b, &full[s], kb * kBK, c.n * kBN, c.e);
+              load_3d<kPair>(db, &tm_b, bar, kb * kBK, n0, c.e);
             }
           }
-          ++issued;
+        }
+        __syncwarp();
+        if (own_tail) {
+          tail_seen |= 1u << s;
+          tail_last = (tail_last & ~(1u << s)) | (tail_next & (1u << s));
+          tail_next ^= 1u << s;
+        }
+        ++issued;
+        if (++s == a.stages) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    // The whole warp walks the ring; lane 0 issues, and in weight mode all
-    // lanes zero the rows of a group's last block that belong to no one.
-    int consumed = 0, filled = 0;  // blocks taken from the ring, accumulators filled
+    // The whole warp walks the ring; one lane issues (the leader's, of a pair),
+    // and in weight mode all lanes zero the rows of a group's last block that
+    // belong to no one (the second CTA's warp does only that).
+    int s = 0, consumed = 0, filled = 0;  // ring stage, blocks taken, accumulators filled
+    uint32_t phase = 0, tail_next = 0;
     bool stop = false;
+    const uint64_t ring_a = operand_desc<S::kAcrossA>(smem_addr(smem));
+    const uint64_t ring_b = operand_desc<S::kAcrossB>(smem_addr(smem) + kABytes);
+    auto zero_rows = [&](int have) {
+      const int chunks = (kBK - have) * 8;  // 16-byte chunks of one box
+      uint8_t* base = smem + s * a.stage_bytes + have * 128;
+#pragma unroll 1
+      for (int box = 0; box < kBM / 64 + b_boxes; ++box)
+        for (int i = lane; i < chunks; i += 32)
+          *reinterpret_cast<uint4*>(base + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_shared();
+      __syncwarp();
+    };
     for (long long t = first_tile; t < total && !stop; t += step) {
       const Tile c = tile_at(t);
-      const int width = min(kBN, (p.n - c.n * kBN + 15) & ~15);
-      const uint32_t idesc = idesc_bf16_f32(kBM, width) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
+      const uint32_t idesc =
+          idesc_bf16_f32(kTileM, width_of(c)) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
       for (int k0 = c.kb0; k0 < c.kb1 && !stop; k0 += S::kWeight ? kChainBlocks : c.kb1 - c.kb0, ++filled) {
         const int acc = filled & 1;
-        if (!mbar_wait(&tempty[acc], ((filled >> 1) & 1) ^ 1, abort_flag)) {
-          stop = true;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * kBN;
-        const int k1 = S::kWeight ? min(k0 + kChainBlocks, c.kb1) : c.kb1;
-        for (int kb = k0; kb < k1; ++kb) {
-          const int s = consumed % kStages;
-          if (!mbar_wait(&full[s], (consumed / kStages) & 1, abort_flag)) {
+        if (leader || !kPair) {
+          if (!mbar_wait(&tempty[acc], ((filled >> 1) & 1) ^ 1, abort_flag)) {
             stop = true;
             break;
           }
-          if constexpr (S::kWeight) {
-            const int have = c.rows.y - c.rows.x - kb * kBK;
-            if (have < kBK) {
-              const int chunks = (kBK - have) * 8;  // 16-byte chunks of one box
-#pragma unroll 1
-              for (int box = 0; box < (kBM + kBN) / 64; ++box) {
-                uint8_t* base =
-                    box < kBM / 64 ? sA + s * kABytes + box * kBoxBytes : sB + s * kBBytes + (box - kBM / 64) * kBoxBytes;
-                for (int i = lane; i < chunks; i += 32)
-                  *reinterpret_cast<uint4*>(base + have * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_shared();
-              __syncwarp();
-            }
-          }
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t ta = smem_addr(sA + s * kABytes), tb = smem_addr(sB + s * kBBytes);
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              umma_bf16(d_tmem, operand_desc<S::kAcrossA>(ta, kk), operand_desc<S::kAcrossB>(tb, kk), idesc,
-                        (kb != k0) || (kk != 0));
-            umma_commit(&empty[s]);
-          }
-          __syncwarp();
-          ++consumed;
+          tc_fence_after();
         }
-        if (!stop && lane == 0) umma_commit(&tfull[acc]);
+        const uint32_t d_tmem = tmem + acc * kBN;
+        const int k1 = S::kWeight ? min(k0 + kChainBlocks, c.kb1) : c.kb1;
+        for (int kb = k0; kb < k1; ++kb) {
+          const int have = S::kWeight ? rows_in(c, kb) : kBK;
+          bool ok = true;
+          if (kPair && !leader) {
+            if (have < kBK) {
+              ok = mbar_wait(&tails[s], (tail_next >> s) & 1, abort_flag);
+              if (ok) {
+                zero_rows(have);
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&zeroed[s]), 0));
+              }
+              tail_next ^= 1u << s;
+            }
+          } else {
+            ok = mbar_wait(&full[s], phase, abort_flag);
+            if (ok && have < kBK) {
+              zero_rows(have);
+              if constexpr (kPair) {
+                ok = mbar_wait(&zeroed[s], (tail_next >> s) & 1, abort_flag);
+                fence_acq_rel_cluster();
+                tail_next ^= 1u << s;
+              }
+            }
+            if (ok && elect_one()) {
+              // descriptors hold addresses in 16-byte units, and no sum of them leaves its field
+              const uint32_t at = s * (a.stage_bytes >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                const uint64_t da = ring_a + (at + kk * (S::kAcrossA ? 2048 >> 4 : 32 >> 4));
+                const uint64_t db = ring_b + (at + kk * (S::kAcrossB ? 2048 >> 4 : 32 >> 4));
+                const uint32_t add = (kb != k0) || (kk != 0);
+                if constexpr (kPair)
+                  umma_bf16_pair(d_tmem, da, db, idesc, add);
+                else
+                  umma_bf16(d_tmem, da, db, idesc, add);
+              }
+              if constexpr (kPair)
+                umma_commit_pair_all(&empty[s], 0x3);
+              else
+                umma_commit(&empty[s]);
+            }
+            __syncwarp();
+          }
+          if (!ok) {
+            stop = true;
+            break;
+          }
+          ++consumed;
+          if (++s == a.stages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (!stop && elect_one()) {
+          if constexpr (kPair) {
+            if (leader) umma_commit_pair_all(&tfull[acc], 0x3);
+          } else {
+            umma_commit(&tfull[acc]);
+          }
+        }
         __syncwarp();
       }
     }
-    if (lane == 0) {
-      if (stop) *abort_flag = 1;
+    __syncwarp();
+    if (elect_one()) {
+      if (stop) raise_abort();
       *consumed_slot = consumed;
-      umma_commit(drain);
-      mbar_wait(drain, 0, nullptr);
+      if (leader || !kPair) {
+        if constexpr (kPair)
+          umma_commit_pair(drain);
+        else
+          umma_commit(drain);
+        mbar_wait(drain, 0, nullptr);
+      }
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;            // TMEM lane quadrant this warp may read
-    const int half = (warp - 2) >> 2;  // which half of the tile's columns it drains
+    const int q = warp & 3;  // TMEM lane quadrant this warp may read
+    // its 32-column blocks of the tile: the first or the second half
+    const int blocks = a.bn / 32, half = (warp - 2) >> 2;
+    const int b_first = half * ((blocks + 1) / 2), b_end = half ? blocks : (blocks + 1) / 2;
     uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
     float* my_bias = s_bias + (warp - 2) * 32;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     int filled = 0;
     auto wait_acc = [&]() {
       if (!mbar_wait(&tfull[filled & 1], (filled >> 1) & 1, abort_flag)) {
-        *abort_flag = 1;
+        raise_abort();
         return false;
       }
       tc_fence_after();
@@ -437,7 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto free_acc = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[filled & 1]);
+      if (lane == 0) {
+        if constexpr (kPair)
+          mbar_arrive_cluster(mapa_shared(smem_addr(&tempty[filled & 1]), 0));
+        else
+          mbar_arrive(&tempty[filled & 1]);
+      }
       ++filled;
     };
     // a partial tile into the operand ring, which nothing reads any more:
@@ -451,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (long long t = first_tile; t < total; t += step) {
       const Tile c = tile_at(t);
-      const int row0 = S::kWeight ? c.m * kBM + q * 32 : c.rows.x + c.m * kBM + q * 32;
+      const int m0 = c.m * kTileM + (kPair ? static_cast<int>(rank) * kBM : 0) + q * 32;
+      const int row0 = S::kWeight ? m0 : c.rows.x + m0;
       const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;  // rows from row0 to the end
       if constexpr (S::kWeight) {
         float f[4][32];
@@ -462,9 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int k0 = c.kb0; k0 < c.kb1; k0 += kChainBlocks) {
           if (!(ok = wait_acc())) break;
-          const uint32_t tbase = tmem + (filled & 1) * kBN + lanes + half * (kBN / 2);
+          const uint32_t tbase = tmem + (filled & 1) * kBN + lanes + b_first * 32;
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
+            if (b_first + (b >> 1) >= b_end) break;
             uint32_t v[16];
             tmem_ld16(tbase + b * 16, v);
             tmem_ld_wait();
@@ -476,31 +620,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int c32 = half * 4 + b, n0 = c.n * kBN + c32 * 32;
+          const int c32 = b_first + b, n0 = c.n * a.bn + c32 * 32;
+          if (c32 >= b_end) break;
           if constexpr (kSplit) {
             keep_partial(c32, f[b]);
           } else {
-            if (n0 < p.n && left > 0) finish_weight(a, f[b], c.e, row0 + lane, row0, n0, stg, lane, &tm_d);
+            if (n0 < p.n && left > 0) finish_block<kMode>(a, f[b], c, row0, left, n0, stg, my_bias, lane, &tm_d, &tm_p);
           }
         }
       } else {
         if (!wait_acc()) break;
         const uint32_t tbase = tmem + (filled & 1) * kBN + lanes;
 #pragma unroll 1
-        for (int c0 = half * (kBN / 2); c0 < (half + 1) * (kBN / 2); c0 += 32) {
-          const int n0 = c.n * kBN + c0;
+        for (int c32 = b_first; c32 < b_end; ++c32) {
+          const int n0 = c.n * a.bn + c32 * 32;
           if (n0 >= p.n || left <= 0) break;
           uint32_t v[32];
           float f[32];
-          tmem_ld32(tbase + c0, v);
+          tmem_ld32(tbase + c32 * 32, v);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
           if constexpr (kSplit)
-            keep_partial(c0 / 32, f);
+            keep_partial(c32, f);
           else
-            finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left,
-                                                     a.tma_store && left >= 32, stg, my_bias, lane, &tm_d, &tm_p);
+            finish_block<kMode>(a, f, c, row0, left, n0, stg, my_bias, lane, &tm_d, &tm_p);
         }
         free_acc();
       }
@@ -509,16 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   if constexpr (kSplit) {
     cluster_sync();  // every partial tile is in place
-    if (warp >= 2 && warp < 2 + kEpiWarps && first_tile < total && !*abort_flag) {
+    if (warp >= 2 && first_tile < total && !*abort_flag) {
       const Tile c = tile_at(first_tile);
       uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
       float* my_bias = s_bias + (warp - 2) * 32;
-      // 32 blocks of 32 x 32 shared out over the cluster's epilogue warps
+      // the tile's blocks of 32 x 32 shared out over the cluster's epilogue warps
 #pragma unroll 1
-      for (int b = part * kEpiWarps + warp - 2; b < (kBN / 32) * 4; b += split * kEpiWarps) {
+      for (int b = rank * kEpiWarps + warp - 2; b < (a.bn / 32) * 4; b += split * kEpiWarps) {
         const int q = b & 3, c32 = b >> 2;
-        const int n0 = c.n * kBN + c32 * 32;
-        const int row0 = S::kWeight ? c.m * kBM + q * 32 : c.rows.x + c.m * kBM + q * 32;
+        const int n0 = c.n * a.bn + c32 * 32;
+        const int row0 = (S::kWeight ? 0 : c.rows.x) + c.m * kBM + q * 32;
         const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;
         if (n0 >= p.n || left <= 0) continue;
         const uint32_t row = smem_addr(smem) + b * 4096 + lane * 128;
@@ -536,11 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) f[4 * j + i] += g[i];
           }
         }
-        if constexpr (S::kWeight)
-          finish_weight(a, f, c.e, row0 + lane, row0, n0, stg, lane, &tm_d);
-        else
-          finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left,
-                                                   a.tma_store && left >= 32, stg, my_bias, lane, &tm_d, &tm_p);
+        finish_block<kMode>(a, f, c, row0, left, n0, stg, my_bias, lane, &tm_d, &tm_p);
       }
     }
     cluster_sync();  // nobody leaves while a peer reads its shared memory
@@ -552,13 +692,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (*abort_flag) {
     if (threadIdx.x == 0) report_status(p.status, MOE_STATUS_TIMEOUT);
+    // loads issued but never consumed must land before the CTA leaves
     if (warp == 0 && lane == 0) {
-      // loads issued but never consumed must land before the CTA leaves
-      for (int i = *consumed_slot; i < issued; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr);
+      if (leader || !kPair)
+        for (int i = *consumed_slot; i < issued; ++i) mbar_wait(&full[i % a.stages], (i / a.stages) & 1, nullptr);
+      for (int s = 0; s < a.stages; ++s)
+        if ((tail_seen >> s) & 1) mbar_wait(&tails[s], (tail_last >> s) & 1, nullptr);
     }
   }
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if constexpr (kPair)
+    cluster_sync();  // neither CTA leaves while the pair's MMAs or signals may still touch it
+  else
+    __syncthreads();
+  if (warp == 1) {
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, kTmemCols);
+    else
+      tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 // A tensor map of up to three dimensions (contiguous first), strides in
@@ -588,28 +739,95 @@ bool store_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, u
                 CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-template <MatmulMode kMode, bool kSplit>
+template <MatmulMode kMode, Form kForm>
 cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const CUtensorMap& tp,
-                         const TcArgs& t, unsigned grid, unsigned split, cudaStream_t s) {
+                         const TcArgs& t, long long grid, int cluster, cudaStream_t s) {
   using S = Shape<kMode>;
-  auto* kernel = matmul_tc_kernel<kMode, kSplit>;
+  auto* kernel = matmul_tc_kernel<kMode, kForm>;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
-  return launch_kernel(kernel, dim3(grid), dim3(kThreads), S::kSmem, s, false, split, ta, tb, td, tp, t);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, s, false,
+                       static_cast<unsigned>(cluster), ta, tb, td, tp, t);
+}
+
+// How a product is cut up.
+struct Choice {
+  Form form;
+  int bn, split;
+};
+
+struct Problem {
+  bool weight;
+  long long rows;  // tiled rows: of D in all groups, or of one group's D (weight mode)
+  int groups, n, blocks;
+};
+
+// Row tiles of `tile` rows: as many as there can be, however the rows fall to
+// the groups, and as many as expected (half a tile of padding a group).
+long long most_tiles(const Problem& q, int tile) {
+  const long long t = (q.rows + tile - 1) / tile;
+  return q.weight ? t * q.groups : t + q.groups - 1;
+}
+double expected_tiles(const Problem& q, int tile) {
+  if (q.weight || q.groups == 1) return static_cast<double>(most_tiles(q, tile));
+  return q.rows / static_cast<double>(tile) + 0.5 * static_cast<double>(std::min<long long>(q.groups, q.rows));
+}
+
+// The cut with the least estimated time on the busiest SM, in nanoseconds: a
+// block of 64 along the reduction costs what it measured on B200 with all SMs
+// busy (2048 rows, 9 column tiles, k 4096 to 8192; forward, wgrad):
+//            bn 256     192        128        64
+//   kPair    374, 384   262, 341   214, 294   203, 327
+//   kSingle  413, 441   341, 379   265, 318   221, 319
+// (narrow tiles are bound by the issue of loads and MMAs, wide ones by the
+// tensor pipe at the clock that the power limit leaves). A tile costs about
+// 500 more, a pair's start 2000, a split's exchange 1500.
+Choice choose_tiles(const Problem& q, int sms) {
+  Choice best{Form::kSingle, kBN, 1};
+  double least = 1e300;
+  auto consider = [&](Form form, int bn, int split, double tiles, int units, double block, double once) {
+    const double waves = std::ceil(tiles / units - 1e-9);
+    const double time = waves * ((q.blocks + split - 1) / split * block + 500) + once;
+    if (time < least) {
+      least = time;
+      best = {form, bn, split};
+    }
+  };
+  for (int bn = kBN; bn >= 64; bn -= 32) {
+    if (bn - 32 >= q.n && bn > 64) continue;  // wider than the matrix
+    const double n_tiles = (q.n + bn - 1) / bn;
+    const double pair = q.weight ? 210 + 0.7 * bn : std::max(1.42 * bn, 160 + 0.45 * bn);
+    const double single = (q.weight ? 210 : 165) + 0.9 * bn;
+    consider(Form::kPair, bn, 1, expected_tiles(q, 256) * n_tiles, sms / 2, pair, 2000);
+    consider(Form::kSingle, bn, 1, expected_tiles(q, 128) * n_tiles, sms, single, 0);
+    for (int split = 2; split <= 8; split *= 2)
+      if (most_tiles(q, 128) * n_tiles * split <= sms && q.blocks >= 2 * split)
+        consider(Form::kSplit, bn, split, 1, 1, single, 1500);
+  }
+  return best;
 }
 
 template <MatmulMode kMode>
 cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   using S = Shape<kMode>;
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  const int sms = device_sm_count();
+  const int depth = S::kWeight ? (a.rows + a.groups - 1) / a.groups : a.k;
+  const Problem q{S::kWeight, S::kWeight ? a.m : a.rows, a.groups, a.n, (depth + kBK - 1) / kBK};
+  const Choice choice = choose_tiles(q, sms);
+  const bool pair = choice.form == Form::kPair;
+  const int tile_m = pair ? 256 : 128, b_cols = pair ? choice.bn / 2 : choice.bn;
   CUtensorMap ta, tb, td{}, tp{};
   TcArgs t{};
   t.p = a;
-  t.n_tiles = (a.n + kBN - 1) / kBN;
+  t.bn = choice.bn;
+  t.n_tiles = (a.n + t.bn - 1) / t.bn;
+  t.m_tiles = S::kWeight ? (a.m + tile_m - 1) / tile_m : 0;
+  t.stage_bytes = kABytes + (S::kAcrossB ? (b_cols + 63) / 64 * kBoxBytes : b_cols * kBK * 2);
+  t.stages = std::min<int>(kMaxStages, kRingBytes / t.stage_bytes);
   bool ok;
   if constexpr (S::kWeight) {
-    t.m_tiles = (a.m + kBM - 1) / kBM;
     t.band = 16;
     ok = load_map(&ta, a.a, a.m, a.rows, a.lda, 0, 0, 64) && load_map(&tb, a.b, a.n, a.rows, a.ldb, 0, 0, 64);
     t.tma_store = a.ldd % 4 == 0;
@@ -622,25 +840,25 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
     }
   } else {
     // a band of row tiles holds about 64 MB of A, so that it stays in L2 while the weights stream past it
-    const long long tile_bytes = 2LL * kBM * a.k;
-    t.band = 8;
-    while (t.band < 32 && t.band * 2 * tile_bytes <= (64LL << 20)) t.band *= 2;
+    const long long tile_bytes = 2LL * tile_m * a.k;
+    t.band = pair ? 4 : 8;
+    while (t.band < (pair ? 16 : 32) && t.band * 2 * tile_bytes <= (64LL << 20)) t.band *= 2;
     constexpr bool fwd = kMode == MatmulMode::kForward;
     ok = load_map(&ta, a.a, a.k, a.rows, a.lda, 0, 0, kBM) &&
-         load_map(&tb, a.b, fwd ? a.k : a.n, fwd ? a.n : a.k, a.ldb, a.groups, a.b_stride, fwd ? kBN : 64) &&
+         load_map(&tb, a.b, fwd ? a.k : a.n, fwd ? a.n : a.k, a.ldb, a.groups, a.b_stride, fwd ? b_cols : 64) &&
          store_map(&td, a.d, a.n, a.rows, a.ldd) && (!a.preact || store_map(&tp, a.preact, a.n, a.rows, a.ldz));
     t.tma_store = 1;
   }
   if (!ok) return cudaErrorInvalidValue;
-  // an upper bound of the row tiles, however the rows fall to the groups
-  const long long m_tiles = S::kWeight ? static_cast<long long>(a.groups) * t.m_tiles : (a.rows + kBM - 1LL) / kBM + a.groups - 1;
-  const long long tiles = m_tiles * t.n_tiles;
-  const int sms = device_sm_count();
-  const int blocks = ((S::kWeight ? a.rows / a.groups : a.k) + kBK - 1) / kBK;
-  unsigned split = 1;
-  while (split < 8 && tiles * split * 2 <= sms && blocks >= static_cast<int>(split) * 4) split *= 2;
-  if (split > 1) return launch_tiles<kMode, true>(ta, tb, td, tp, t, static_cast<unsigned>(tiles * split), split, s);
-  return launch_tiles<kMode, false>(ta, tb, td, tp, t, static_cast<unsigned>(std::min<long long>(tiles, sms)), 1, s);
+  const long long tiles = most_tiles(q, tile_m) * t.n_tiles;
+  switch (choice.form) {
+    case Form::kPair:
+      return launch_tiles<kMode, Form::kPair>(ta, tb, td, tp, t, 2 * std::min<long long>(tiles, sms / 2), 2, s);
+    case Form::kSplit:
+      return launch_tiles<kMode, Form::kSplit>(ta, tb, td, tp, t, tiles * choice.split, choice.split, s);
+    default:
+      return launch_tiles<kMode, Form::kSingle>(ta, tb, td, tp, t, std::min<long long>(tiles, sms), 1, s);
+  }
 }
 
 }  // namespace

@@ -195,6 +195,59 @@ def test_dense(dt, m, k, n):
     close(db, want_b[0], rounded(sum_error(m, scale_b[0]), want_b[0], F32), "db")
 
 
+LARGE = [  # (rows of each group, k, n, pad): enough tiles for every way the bf16 kernel cuts a product up
+    ([4099], 1032, 1408, 0), ([2500], 2048, 2048, 0), ([640], 4096, 264, 0), ([150], 6000, 640, 0), ([20000], 72, 160, 0),
+    ([600, 0, 1, 257, 1500, 63, 1030, 255], 520, 1400, 0), ([2048, 2047, 2049, 0, 300], 640, 1288, 0),
+    ([700, 900, 1200, 0, 31, 2000], 1001, 1111, 8), ([130] * 40, 264, 776, 0),
+    ([9, 70, 200, 0, 1, 3, 64, 65] * 24, 200, 328, 0),
+]
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("sizes,k,n,pad", LARGE)
+def test_large(dt, sizes, k, n, pad):
+    """Products of many tiles (the oracle's formulas evaluated in 64 bits on the GPU)."""
+    g = torch.Generator().manual_seed(14)
+    off = offsets_of(sizes, first=3)
+    rows, E = off[-1] + 5, len(sizes)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    x, dy = matrix((rows, k), dt, g, pad, poison=True), matrix((rows, n), dt, g, pad, poison=True)
+    w = matrix((E, n, k), dt, g, pad, 1 / math.sqrt(k), poison=True)
+    bias, res, z = torch.randn((E, n), generator=g).to(DEV), matrix((rows, n), dt, g, pad), matrix((rows, k), dt, g, pad)
+    for t in (x, dy):
+        t[:3], t[off[-1]:] = math.nan, math.nan
+    pre, y = matrix((rows, n), dt, g, pad), matrix((rows, n), dt, g, pad)
+    dx, before = matrix((rows, k), dt, g, pad), y.clone()
+    db = torch.full((E, n), math.nan, device=DEV)
+    dw = torch.full((E, n, k), math.nan, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    M.moe_grouped_gemm(x, o, w, bias=bias, act="gelu", residual=res, preact=pre, y=y, status=status)
+    M.moe_grouped_gemm_dgrad(dy, o, w, z=z, act="silu", dx=dx, status=status)
+    M.moe_grouped_gemm_wgrad(dy, o, x, dw=dw, dbias=db, status=status)
+    assert int(status.item()) == 0
+    assert torch.equal(y[:3], before[:3]) and torch.equal(y[off[-1]:], before[off[-1]:])
+
+    def near(got, want, tol, t, what):
+        off_by = (got.double() - want).abs() - rounded(tol, want, t)
+        assert torch.isfinite(got).all() and bool((off_by <= 0).all()), (what, float(off_by.max()))
+
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        xd, dd, wd, rd = x[a:b].double(), dy[a:b].double(), w[e].double(), res[a:b].double()
+        u, err = xd @ wd.T + bias[e].double(), sum_error(k, xd.abs() @ wd.abs().T + bias[e].double().abs())
+        near(pre[a:b], u, err, dt, "preact")
+        v = R.act(u, "gelu")
+        err = 1.13 * err + 1e-5 * v.abs() + 1e-6 * u.abs() + 2.0 ** -24 * (v.abs() + rd.abs())
+        near(y[a:b], v + rd, err, dt, "y")
+        s = R.act_slope(z[a:b], "silu")
+        v, err = (dd @ wd) * s, sum_error(n, dd.abs() @ wd.abs())
+        near(dx[a:b], v, 1.13 * err + 1e-5 * (dd @ wd).abs(), dt, "dx")
+        # 512 rows an accumulator, then one rounding each
+        near(dw[e], dd.T @ xd, sum_error(min(b - a, 512) / 16 + (b - a) / 512 if dt == BF16 else b - a, dd.abs().T @ xd.abs()),
+             F32, "dw")
+        near(db[e], dd.sum(0), sum_error(b - a, dd.abs().sum(0)), F32, "db")
+
+
 def test_other_groups_infinities_stay_theirs():
     """Infinities in one group's rows and weights reach no other group's outputs."""
     for dt in (F32, BF16):
