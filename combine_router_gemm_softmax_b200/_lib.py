@@ -472,21 +472,28 @@ def _act(act) -> int:
         raise ValueError(f"act: {act!r} is none of {', '.join(_ACTS)}") from None
 
 
-def _strided(t, shape, dtype, device, name):
+def _refuse(t, shape, dtype, index, name):
+    """The error of a tensor that is not `shape` of `dtype` on device `index`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
+    raise ValueError(f"{name}: on {t.device}, not on {torch.device('cuda', index) if index >= 0 else 'cpu'}")
+
+
+def _strided(t, shape, dtype, index, name):
     """Checks a matrix whose rows may lie apart (unit stride along the last
     axis) and returns its address and row stride; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, shape, dtype, index, name)
     st = t.stride()
-    rows, width = shape[-2], shape[-1]
-    ld = st[-2] if rows > 1 else (width + 7) // 8 * 8  # a single row's stride leads nowhere
-    if (width > 1 and st[-1] != 1) or ld < width:
+    width = shape[-1]
+    ld = st[-2] if shape[-2] > 1 else (width + 7) // 8 * 8  # a single row's stride leads nowhere
+    if (st[-1] != 1 and width > 1) or ld < width:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {st})")
     return t.data_ptr(), ld
 
@@ -498,42 +505,38 @@ def _matrix(rows, width, dtype, device):
     return t if wide == width else t[:, :width]
 
 
-def _plain(t, shape, dtype, device, name):
+def _plain(t, shape, dtype, index, name):
     """Address of a contiguous tensor of this shape; None for None."""
     if t is None:
         return None
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, shape, dtype, index, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
 def _first(t, dims, name):
-    """Device and MOE_DTYPE_* of a call's leading operand."""
+    """Device index and MOE_DTYPE_* of a call's leading operand."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name}: must be on a CUDA device")
     if t.dim() != dims:
         raise ValueError(f"{name}: {t.dim()} axes, not {dims}")
     try:
-        return t.device, _GEMM_DTYPES[t.dtype]
+        return index, _GEMM_DTYPES[t.dtype]
     except KeyError:
         raise ValueError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32") from None
 
 
-def _enqueue(fn, device, stream, *args):
+def _enqueue(fn, index, stream, *args):
     """Calls the entry point on `stream` (default: the device's current one),
     with the tensors' device current."""
     f = getattr(_lib or lib(), fn)
-    index = device.index
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         code = f(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -542,10 +545,10 @@ def _enqueue(fn, device, stream, *args):
         _rc(fn, code)
 
 
-def _weights(w, groups, n, k, dtype, device):
+def _weights(w, groups, n, k, dtype, index):
     """Address, row stride and group stride of w [groups, n, k] (or [n, k])."""
-    p, ld = _strided(w, (groups, n, k) if w.dim() == 3 else (n, k), dtype, device, "w")
-    if w.dim() == 2 or groups <= 1:
+    p, ld = _strided(w, (groups, n, k) if w.dim() == 3 else (n, k), dtype, index, "w")
+    if groups <= 1:
         return p, ld, n * ld
     between = w.stride(0)
     if between < (n - 1) * ld + k:
@@ -553,24 +556,27 @@ def _weights(w, groups, n, k, dtype, device):
     return p, ld, between
 
 
-def _forward(fn, x, offsets, w, bias, act, residual, preact, y, status, stream):
+def _forward(fn, dims, x, offsets, w, bias, act, residual, preact, y, status, stream):
     dev, dt = _first(x, 2, "x")
-    _first(w, 2 if fn == "moe_linear" else 3, "w")
+    if w.dim() != dims:
+        raise ValueError(f"w: {w.dim()} axes, not {dims}")
     rows, k = x.shape
-    n = w.shape[-2]
-    groups = w.shape[0] if w.dim() == 3 else 1
+    shape = w.shape
+    n = shape[-2]
+    groups = shape[0] if dims == 3 else 1
     tdt = x.dtype
-    px, ldx = _strided(x, (rows, k), tdt, dev, "x")
+    out = (rows, n)
+    px, ldx = _strided(x, x.shape, tdt, dev, "x")
     pw, ldw, ws = _weights(w, groups, n, k, tdt, dev)
-    pb = _plain(bias, w.shape[:-1], torch.float32, dev, "bias")
-    pr, ldr = _strided(residual, (rows, n), tdt, dev, "residual")
-    pz, ldz = _strided(preact, (rows, n), tdt, dev, "preact")
+    pb = _plain(bias, shape[:-1], torch.float32, dev, "bias") if bias is not None else None
+    pr, ldr = _strided(residual, out, tdt, dev, "residual")
+    pz, ldz = _strided(preact, out, tdt, dev, "preact")
     if y is None:
-        y = _matrix(rows, n, tdt, dev)
-    py, ldy = _strided(y, (rows, n), tdt, dev, "y")
+        y = _matrix(rows, n, tdt, x.device)
+    py, ldy = _strided(y, out, tdt, dev, "y")
     cfg = MoeGemmConfig(rows, n, k, groups, dt, _act(act), ldx, ldw, ws, ldy, ldr, ldz)
     ps = _plain(status, (1,), torch.int32, dev, "status")
-    if fn == "moe_linear":
+    if dims == 2:
         _enqueue(fn, dev, stream, cfg, px, pw, pb, pr, pz, py, ps)
     else:
         _enqueue(fn, dev, stream, cfg, px, _plain(offsets, (groups + 1,), torch.int32, dev, "offsets"), pw, pb, pr, pz,
@@ -578,23 +584,25 @@ def _forward(fn, x, offsets, w, bias, act, residual, preact, y, status, stream):
     return y
 
 
-def _dgrad(fn, dy, offsets, w, z, act, residual, dx, status, stream):
+def _dgrad(fn, dims, dy, offsets, w, z, act, residual, dx, status, stream):
     dev, dt = _first(dy, 2, "dy")
-    _first(w, 2 if fn == "moe_linear_dgrad" else 3, "w")
+    if w.dim() != dims:
+        raise ValueError(f"w: {w.dim()} axes, not {dims}")
     rows, n = dy.shape
     k = w.shape[-1]
-    groups = w.shape[0] if w.dim() == 3 else 1
+    groups = w.shape[0] if dims == 3 else 1
     tdt = dy.dtype
-    pdy, ldy = _strided(dy, (rows, n), tdt, dev, "dy")
+    out = (rows, k)
+    pdy, ldy = _strided(dy, dy.shape, tdt, dev, "dy")
     pw, ldw, ws = _weights(w, groups, n, k, tdt, dev)
-    pz, ldz = _strided(z, (rows, k), tdt, dev, "z")
-    pr, ldr = _strided(residual, (rows, k), tdt, dev, "residual")
+    pz, ldz = _strided(z, out, tdt, dev, "z")
+    pr, ldr = _strided(residual, out, tdt, dev, "residual")
     if dx is None:
-        dx = _matrix(rows, k, tdt, dev)
-    pdx, ldx = _strided(dx, (rows, k), tdt, dev, "dx")
+        dx = _matrix(rows, k, tdt, dy.device)
+    pdx, ldx = _strided(dx, out, tdt, dev, "dx")
     cfg = MoeGemmConfig(rows, n, k, groups, dt, _act(act), ldx, ldw, ws, ldy, ldr, ldz)
     ps = _plain(status, (1,), torch.int32, dev, "status")
-    if fn == "moe_linear_dgrad":
+    if dims == 2:
         _enqueue(fn, dev, stream, cfg, pdy, pw, pz, pr, pdx, ps)
     else:
         _enqueue(fn, dev, stream, cfg, pdy, _plain(offsets, (groups + 1,), torch.int32, dev, "offsets"), pw, pz, pr,
@@ -602,22 +610,21 @@ def _dgrad(fn, dy, offsets, w, z, act, residual, dx, status, stream):
     return dx
 
 
-def _wgrad(fn, dy, offsets, x, groups, dw, dbias, status, stream):
+def _wgrad(fn, dims, dy, offsets, x, groups, dw, dbias, status, stream):
     dev, dt = _first(dy, 2, "dy")
-    rows, n = dy.shape
     _first(x, 2, "x")
+    rows, n = dy.shape
     k = x.shape[1]
-    pdy, ldy = _strided(dy, (rows, n), dy.dtype, dev, "dy")
+    pdy, ldy = _strided(dy, dy.shape, dy.dtype, dev, "dy")
     px, ldx = _strided(x, (rows, k), dy.dtype, dev, "x")
-    dense = fn == "moe_linear_wgrad"
-    shape = (n, k) if dense else (groups, n, k)
+    shape = (n, k) if dims == 2 else (groups, n, k)
     if dw is None:
-        dw = torch.empty(shape, dtype=torch.float32, device=dev)
+        dw = torch.empty(shape, dtype=torch.float32, device=dy.device)
     pdw = _plain(dw, shape, torch.float32, dev, "dw")
     pdb = _plain(dbias, shape[:-1], torch.float32, dev, "dbias")
     cfg = MoeGemmConfig(rows, n, k, groups, dt, MOE_ACT_NONE, ldx, 0, 0, ldy, 0, 0)
     ps = _plain(status, (1,), torch.int32, dev, "status")
-    if dense:
+    if dims == 2:
         _enqueue(fn, dev, stream, cfg, pdy, px, pdw, pdb, ps)
     else:
         _enqueue(fn, dev, stream, cfg, pdy, _plain(offsets, (groups + 1,), torch.int32, dev, "offsets"), px, pdw, pdb,
@@ -634,37 +641,37 @@ def moe_grouped_gemm(x, offsets, w, bias=None, act="none", residual=None, preact
     receives the argument of act. Rows of matrices may lie apart (bf16 row
     strides: multiples of 8). Rows outside every group are left as they were
     (uninitialised in a y made here). Returns y."""
-    return _forward("moe_grouped_gemm", x, _given(offsets), w, bias, act, residual, preact, y, status, stream)
+    return _forward("moe_grouped_gemm", 3, x, _given(offsets), w, bias, act, residual, preact, y, status, stream)
 
 
 def moe_grouped_gemm_dgrad(dy, offsets, w, z=None, act="none", residual=None, dx=None, status=None, stream=None):
     """dx[r] = act'(z[r]) * (dy[r] w[e]) + residual[r]: the input gradient,
     through the activation x = act(z) that made the input when z [rows, k] is
     given. Returns dx [rows, k]."""
-    return _dgrad("moe_grouped_gemm_dgrad", dy, _given(offsets), w, z, act, residual, dx, status, stream)
+    return _dgrad("moe_grouped_gemm_dgrad", 3, dy, _given(offsets), w, z, act, residual, dx, status, stream)
 
 
 def moe_grouped_gemm_wgrad(dy, offsets, x, dw=None, dbias=None, status=None, stream=None):
     """dw[e] = dy_e^T x_e (fp32 [E, n, k], E from offsets); dbias [E, n] fp32,
     when given, receives the column sums of dy_e. Returns dw."""
-    return _wgrad("moe_grouped_gemm_wgrad", dy, _given(offsets), x, offsets.numel() - 1, dw, dbias, status, stream)
+    return _wgrad("moe_grouped_gemm_wgrad", 3, dy, _given(offsets), x, offsets.numel() - 1, dw, dbias, status, stream)
 
 
 def moe_linear(x, w, bias=None, act="none", residual=None, preact=None, y=None, status=None, stream=None):
     """y = act(x w^T + bias) + residual for one dense weight w [n, k]; the
     arguments are moe_grouped_gemm's. Returns y [rows, n]."""
-    return _forward("moe_linear", x, None, w, bias, act, residual, preact, y, status, stream)
+    return _forward("moe_linear", 2, x, None, w, bias, act, residual, preact, y, status, stream)
 
 
 def moe_linear_dgrad(dy, w, z=None, act="none", residual=None, dx=None, status=None, stream=None):
     """dx = act'(z) * (dy w) + residual, see moe_grouped_gemm_dgrad."""
-    return _dgrad("moe_linear_dgrad", dy, None, w, z, act, residual, dx, status, stream)
+    return _dgrad("moe_linear_dgrad", 2, dy, None, w, z, act, residual, dx, status, stream)
 
 
 def moe_linear_wgrad(dy, x, dw=None, dbias=None, status=None, stream=None):
     """dw = dy^T x (fp32 [n, k]) and, when dbias [n] is given, the column sums
     of dy. Returns dw."""
-    return _wgrad("moe_linear_wgrad", dy, None, x, 1, dw, dbias, status, stream)
+    return _wgrad("moe_linear_wgrad", 2, dy, None, x, 1, dw, dbias, status, stream)
 
 
 def _given(offsets):
@@ -681,7 +688,7 @@ def moe_act_backward(dy, z, act, dz=None, stream=None):
     pdy, ldy = _strided(dy, shape, dy.dtype, dev, "dy")
     pz, ldz = _strided(z, shape, dy.dtype, dev, "z")
     if dz is None:
-        dz = _matrix(*shape, dy.dtype, dev)
+        dz = _matrix(*shape, dy.dtype, dy.device)
     pdz, ldr = _strided(dz, shape, dy.dtype, dev, "dz")
     cfg = MoeGemmConfig(shape[0], shape[1], 1, 1, dt, _act(act), 0, 0, 0, ldy, ldr, ldz)
     _enqueue("moe_act_backward", dev, stream, cfg, pdy, pz, pdz)
@@ -699,7 +706,7 @@ def moe_dropout(x, p, rng=None, offset=0, residual=None, y=None, stream=None):
     px, ldx = _strided(x, shape, x.dtype, dev, "x")
     pr, ldr = _strided(residual, shape, x.dtype, dev, "residual")
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
     py, ldy = _strided(y, shape, x.dtype, dev, "y")
     _enqueue("moe_dropout", dev, stream, shape[0], shape[1], dt, px, ldx, pr, ldr, py, ldy, p,
              _plain(rng, (2,), torch.int64, dev, "rng"), offset)
@@ -721,7 +728,7 @@ def moe_unpermute_combine_dropout(cfg, y_perm, dest_row, topk_gate, p, rng=None,
     pg = _plain(topk_gate, (cfg.T, cfg.k), torch.float32, dev, "topk_gate")
     pr = _plain(residual, (cfg.T, cfg.d), dt, dev, "residual")
     if y is None:
-        y = torch.empty((cfg.T, cfg.d), dtype=dt, device=dev)
+        y = torch.empty((cfg.T, cfg.d), dtype=dt, device=y_perm.device)
     py = _plain(y, (cfg.T, cfg.d), dt, dev, "y")
     _enqueue("moe_unpermute_combine_dropout", dev, stream, cfg, pp, pd, pg, pr, p,
              _plain(rng, (2,), torch.int64, dev, "rng"), offset, py)

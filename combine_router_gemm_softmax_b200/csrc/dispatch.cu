@@ -21,7 +21,6 @@
 // Nothing decides an order with atomics, so the permutation is deterministic.
 // Kernels after the first of a call are launched as programmatic dependents
 // and wait (griddepcontrol.wait) before touching earlier kernels' memory.
-#include "dropout.cuh"
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -462,10 +461,9 @@ constexpr int combine_batch_k(int nk, int k) {
 
 // y[t] from the token's NK kept rows (slot order), one warp: all NK rows of U
 // 16-byte segments per lane are loaded before any is used.
-// `post` then changes each segment's sums before they are rounded.
-template <int DT, int NK, int U, int K, typename Post>
+template <int DT, int NK, int U, int K>
 MOE_DEV void combine_rows(const uint4* __restrict__ y_perm, const int (&dst)[K], const float (&g)[K],
-                          uint4* __restrict__ yrow, int vpr, int lane, int t, const Post& post) {
+                          uint4* __restrict__ yrow, int vpr, int lane) {
   using V = Vec<DT>;
   for (int v0 = 0; v0 < vpr; v0 += 32 * U) {
     uint4 q[NK][U];
@@ -489,56 +487,21 @@ MOE_DEV void combine_rows(const uint4* __restrict__ y_perm, const int (&dst)[K],
         for (int i = 0; i < V::N; ++i) acc[i] = fmaf(g[j], f[i], acc[i]);
       }
       const int v = v0 + u * 32 + lane;
-      if (v < vpr) {
-        post.template apply<V>(acc, t, v, vpr);
-        yrow[v] = V::store(acc);
-      }
+      if (v < vpr) yrow[v] = V::store(acc);
     }
   }
 }
-
-// moe_unpermute_combine: the sums as they are.
-struct CombinePlain {
-  MOE_DEV void start() {}
-  template <typename V>
-  MOE_DEV void apply(float (&)[V::N], int, int, int) const {}
-};
-
-// moe_unpermute_combine_dropout: dropout, then the residual row added.
-struct CombineDropout {
-  DropoutArgs d;
-  const uint4* residual;  // [T, d] or NULL
-  DropoutState s;
-  MOE_DEV void start() {
-    if (d.cut != 0) s = dropout_state(d);
-  }
-  template <typename V>
-  MOE_DEV void apply(float (&acc)[V::N], int t, int v, int vpr) const {
-    float r[V::N];
-    if (residual != nullptr) V::load(__ldcs(residual + static_cast<size_t>(t) * vpr + v), r);
-    if (d.cut != 0) {
-#pragma unroll
-      for (int j = 0; j < V::N / 4; ++j)
-        dropout_quad(d, s, static_cast<uint32_t>(v) * (V::N / 4) + j, static_cast<uint32_t>(t), acc + 4 * j);
-    }
-    if (residual != nullptr) {
-#pragma unroll
-      for (int i = 0; i < V::N; ++i) acc[i] += r[i];
-    }
-  }
-};
 
 // One warp per token: y[t] = sum_j gate[t,j] * y_perm[dest_row[t,j]] in fp32,
 // slots in order 0..k-1, dropped slots skipped. The kept slots are listed
 // first (in slot order) and the loads are batched by their number, so a token
 // that kept few of its k slots still has about 16 loads per lane in flight.
-template <int DT, int K, typename Post>
+template <int DT, int K>
 __global__ void __launch_bounds__(256, kCombineCtasPerSm<K>) combine_kernel(const uint4* __restrict__ y_perm,
                                                       const int32_t* __restrict__ dest_row,
                                                       const float* __restrict__ gate, uint4* __restrict__ y, int T,
-                                                      int vpr, Post post) {
+                                                      int vpr) {
   pdl_wait();
-  post.start();
   const int lane = threadIdx.x & 31;
   const int nw = gridDim.x * (blockDim.x >> 5);
   for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T; t += nw) {
@@ -559,15 +522,11 @@ __global__ void __launch_bounds__(256, kCombineCtasPerSm<K>) combine_kernel(cons
     uint4* yrow = y + static_cast<size_t>(t) * vpr;
     switch (__popc(kept)) {
       case 0:
-        for (int v = lane; v < vpr; v += 32) {
-          float none[Vec<DT>::N] = {};
-          post.template apply<Vec<DT>>(none, t, v, vpr);
-          yrow[v] = Vec<DT>::store(none);
-        }
+        for (int v = lane; v < vpr; v += 32) yrow[v] = make_uint4(0, 0, 0, 0);
         break;
 #define MOE_COMBINE_NK(NKK)                                                              \
   case NKK:                                                                              \
-    if constexpr (NKK <= K) combine_rows<DT, NKK, combine_batch_k(NKK, K), K>(y_perm, dst, g, yrow, vpr, lane, t, post); \
+    if constexpr (NKK <= K) combine_rows<DT, NKK, combine_batch_k(NKK, K), K>(y_perm, dst, g, yrow, vpr, lane); \
     break;
       MOE_COMBINE_NK(1)
       MOE_COMBINE_NK(2)
@@ -584,15 +543,15 @@ __global__ void __launch_bounds__(256, kCombineCtasPerSm<K>) combine_kernel(cons
   }
 }
 
-template <int DT, typename Post>
+template <int DT>
 cudaError_t launch_combine_k(const uint4* y_perm, const int32_t* dest_row, const float* gate, uint4* y, int T, int k,
-                             int vpr, int grid, bool pdl, cudaStream_t s, const Post& post) {
+                             int vpr, int grid, bool pdl, cudaStream_t s) {
   cudaError_t err = cudaSuccess;
   switch (k) {
 #define MOE_COMBINE_K(KK)                                                                                       \
   case KK:                                                                                                     \
-    err = launch_kernel(combine_kernel<DT, KK, Post>, dim3(grid), dim3(256), 0, s, pdl, 1, y_perm, dest_row, gate, y, \
-                        T, vpr, post);                                                                         \
+    err = launch_kernel(combine_kernel<DT, KK>, dim3(grid), dim3(256), 0, s, pdl, 1, y_perm, dest_row, gate, y, T, \
+                        vpr);                                                                                  \
     break;
     MOE_COMBINE_K(1)
     MOE_COMBINE_K(2)
@@ -680,34 +639,17 @@ cudaError_t launch_permute(const void* h, size_t row_bytes, const int32_t* idx, 
   return cudaGetLastError();
 }
 
-namespace {
-
-template <typename Post>
-cudaError_t launch_combine_post(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate, void* y,
-                                int T, int k, int d, bool pdl, cudaStream_t s, const Post& post) {
+cudaError_t launch_combine(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate, void* y,
+                           int T, int k, int d, bool pdl, cudaStream_t s, int32_t* status) {
+  (void)status;  // the combine has no wait that could time out
   if (T == 0) return cudaSuccess;
   const int elem = dtype == MOE_DTYPE_BF16 ? 2 : 4;
   const int vpr = d * elem / 16;
   if (dtype == MOE_DTYPE_BF16)
     return launch_combine_k<MOE_DTYPE_BF16>(static_cast<const uint4*>(y_perm), dest_row, gate,
-                                            static_cast<uint4*>(y), T, k, vpr, warp_grid(T), pdl, s, post);
+                                            static_cast<uint4*>(y), T, k, vpr, warp_grid(T), pdl, s);
   return launch_combine_k<MOE_DTYPE_F32>(static_cast<const uint4*>(y_perm), dest_row, gate, static_cast<uint4*>(y),
-                                         T, k, vpr, warp_grid(T), pdl, s, post);
-}
-
-}  // namespace
-
-cudaError_t launch_combine(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate, void* y,
-                           int T, int k, int d, bool pdl, cudaStream_t s, int32_t* status) {
-  (void)status;  // the combine has no wait that could time out
-  return launch_combine_post(dtype, y_perm, dest_row, gate, y, T, k, d, pdl, s, CombinePlain{});
-}
-
-cudaError_t launch_combine_dropout(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate,
-                                   const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
-                                   cudaStream_t s) {
-  return launch_combine_post(dtype, y_perm, dest_row, gate, y, T, k, d, false, s,
-                             CombineDropout{drop, static_cast<const uint4*>(residual), {}});
+                                         T, k, vpr, warp_grid(T), pdl, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,163 @@
+// The free products in bf16 for few rows a group (moe_grouped_gemm and
+// moe_linear when tokens are decoded): y[r, j] = fin(sum_i x[r, i] W_e[j, i]).
+//
+// Bound: HBM, the weights of the groups that have rows, each read once. A
+// 128-row tile would leave most of its rows empty and, with one CTA a tile,
+// too few SMs with loads in flight. Here a CTA of 8 warps takes 32 output
+// features (16 where that would be few CTAs) of one group and 8 of its rows; its warps share the
+// reduction, and their sums meet in shared memory in warp order (the same
+// result on every run).
+//
+// The weights go from global memory straight into the fragments of mma.sync
+// (m16n8k16, W as the 16-row operand, the tokens as the 8 columns): a lane
+// reads 16 bytes of a weight row, k = 8 t .. 8 t + 7 of a chunk of 32, and
+// uses them as the k pairs of two MMAs; the token operand is read the same
+// way, so both operands agree on which k a slot holds and no shuffle or shared
+// memory is needed. A warp has 8 KB of weights in flight.
+#include "matmul_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kChunk = 32;  // reduction elements of a step
+
+// Eight elements of a row from p: all of them, or the first `valid`, or none.
+template <bool kStream>
+MOE_DEV uint4 load8(const __nv_bfloat16* p, int valid) {
+  if (valid >= 8) {
+    uint4 q;
+    if constexpr (kStream)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                   : "l"(p));
+    else
+      q = __ldg(reinterpret_cast<const uint4*>(p));
+    return q;
+  }
+  uint32_t h[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < valid) h[i >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[i])) << (16 * (i & 1));
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+MOE_DEV void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// kTiles: 16-feature blocks of a CTA; kWarps: its warps, 16 of which an SM holds.
+template <int kTiles, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) matmul_rows_kernel(const MatmulArgs a) {
+  constexpr int kThreads = 32 * kWarps;
+  constexpr int kFeatures = 16 * kTiles;
+  constexpr int kUnroll = 8 / kTiles;  // chunks in flight
+  __shared__ int2 s_rows[kMaxE];
+  __shared__ int prefix[kMaxE + 1];
+  __shared__ float s_sum[kWarps][8][kFeatures + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  int e = 0, r0 = blockIdx.y * 8, end = a.rows;
+  if (a.offsets != nullptr) {
+    if (warp == 0) build_groups(a.offsets, a.groups, a.rows, 3, s_rows, prefix, blockIdx.y == 0 ? a.status : nullptr, lane);
+    __syncthreads();
+    const int tile = blockIdx.y;
+    if (tile >= prefix[a.groups]) return;
+    e = group_of_tile(prefix, a.groups, tile);
+    r0 = s_rows[e].x + (tile - prefix[e]) * 8;
+    end = s_rows[e].y;
+  }
+  const int have = min(8, end - r0);
+  const int n0 = blockIdx.x * kFeatures;
+  const int g = lane >> 2, t = lane & 3;
+
+  // this warp's chunks of the reduction
+  const int chunks = (a.k + kChunk - 1) / kChunk;
+  const int c0 = static_cast<int>(static_cast<long long>(chunks) * warp / kWarps);
+  const int c1 = static_cast<int>(static_cast<long long>(chunks) * (warp + 1) / kWarps);
+  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.b) + e * a.b_stride + (n0 + g) * a.ldb + t * 8;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.a) + (static_cast<long long>(r0) + g) * a.lda + t * 8;
+  float acc[kTiles][4];
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
+
+  for (int c = c0; c < c1; c += kUnroll) {
+    uint4 qw[kUnroll][2 * kTiles], qx[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = (c + u) * kChunk;
+      const int valid = c + u < c1 ? a.k - k - t * 8 : 0;  // of this lane's eight
+#pragma unroll
+      for (int i = 0; i < 2 * kTiles; ++i)
+        qw[u][i] = load8<true>(w + static_cast<long long>(i) * 8 * a.ldb + k, n0 + g + 8 * i < a.n ? valid : 0);
+      qx[u] = load8<false>(x + k, g < have ? valid : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) {
+        const uint4 &lo = qw[u][2 * m], &hi = qw[u][2 * m + 1];
+        mma(acc[m], lo.x, hi.x, lo.y, hi.y, qx[u].x, qx[u].y);
+        mma(acc[m], lo.z, hi.z, lo.w, hi.w, qx[u].z, qx[u].w);
+      }
+  }
+  // rows g and g + 8 of the 16 features, tokens 2 t and 2 t + 1
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_sum[warp][2 * t + (i & 1)][m * 16 + g + 8 * (i >> 1)] = acc[m][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < have * kFeatures; i += kThreads) {
+    const int token = i / kFeatures, f = i % kFeatures, n = n0 + f;
+    if (n >= a.n) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) v += s_sum[q][token][f];
+    const long long r = static_cast<long long>(r0) + token;
+    if (a.bias != nullptr) v += a.bias[static_cast<size_t>(e) * a.n + n];
+    if (a.preact != nullptr) static_cast<__nv_bfloat16*>(a.preact)[r * a.ldz + n] = __float2bfloat16_rn(v);
+    v = act_of<true>(v, a.act);
+    if (a.residual != nullptr) v += __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[r * a.ldr + n]);
+    static_cast<__nv_bfloat16*>(a.d)[r * a.ldd + n] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int kTiles, int kWarps>
+cudaError_t launch_features(const MatmulArgs& a, long long blocks, cudaStream_t s) {
+  return launch_kernel(matmul_rows_kernel<kTiles, kWarps>,
+                       dim3((a.n + 16 * kTiles - 1) / (16 * kTiles), static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0,
+                       s, true, 1, a);
+}
+
+}  // namespace
+
+// Row blocks: at most, however the rows fall to the groups.
+static long long row_blocks(const MatmulArgs& a) { return (a.rows + 7LL) / 8 + std::min(a.groups, a.rows) - 1; }
+
+// Where this kernel measured faster than the tiles (us, here / there): one
+// block a group (k 4096, n 14336, 1-8 rows 24.1 / 28.1; k 1408, n 2048 3.5 /
+// 8.5; 2 tokens of 8 experts each out of 128 13.4 / 26.1), and several blocks
+// of one group while reading its weights again from L2 stays cheap (k 1408, n
+// 2048, 64 rows: 46 MB of reads 8.0 / 8.8, 96 rows: 69 MB 14.1 / 8.9; k = n =
+// 4096, 24 rows: 100 MB 15.5 / 13.9).
+bool matmul_few_rows(const MatmulArgs& a) {
+  return a.rows <= 8 || 2LL * a.rows <= a.groups || row_blocks(a) * a.n * static_cast<long long>(a.k) <= (24LL << 20);
+}
+
+cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s) {
+  const long long blocks = row_blocks(a);
+  // The cut with the most warps that still fit on the SMs at once (16 each):
+  // with k 4096, n 4096 and one row 16 features x 8 warps take 8.2 us, 32 x 8
+  // 10.1 and 32 x 4 15.5; with n 14336, 26.7, 25.4 and 23.8 us.
+  const long long fit = 16LL * device_sm_count();
+  if ((a.n + 15) / 16 * blocks * 8 <= fit) return launch_features<1, 8>(a, blocks, s);
+  if ((a.n + 31) / 32 * blocks * 8 <= fit) return launch_features<2, 8>(a, blocks, s);
+  return launch_features<2, 4>(a, blocks, s);
+}
+
+}  // namespace moe

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
   uint32_t split, part;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
   part = split > 1 ? cluster_ctarank() : 0;
+  pdl_wait();
   if (threadIdx.x < 32)
     build_groups(a.offsets, a.groups, a.rows, BT == 128 ? 7 : 6, s_rows, prefix, a.status, threadIdx.x);
   __syncthreads();
@@ -261,13 +262,13 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   };
   if (tiles(128) >= sms)
     return launch_kernel(matmul_simt_kernel<kMode, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
-                         dim3(kThreads), 0, s, false, 1, a);
+                         dim3(kThreads), 0, s, true, 1, a);
   const long long t = tiles(64);
   const int depth = kMode == MatmulMode::kWgrad ? a.rows : a.k;
   int split = 1;
   while (split < 8 && t * split * 2 <= 2 * sms && depth / (split * 2) >= 64) split *= 2;
   const long long grid = std::min<long long>(t, 4 * sms) * split;
-  return launch_kernel(matmul_simt_kernel<kMode, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, false,
+  return launch_kernel(matmul_simt_kernel<kMode, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, true,
                        static_cast<unsigned>(split), a);
 }
 
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const T* dy, long long 
   part = split > 1 ? cluster_ctarank() : 0;
   const int e = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n0 = static_cast<int>(blockIdx.x / split) * 128;
+  pdl_wait();
   const int2 g = group_rows(offsets, e, rows);
   const long long have = g.y - g.x;
   const int r0 = g.x + static_cast<int>(have * part / split), r1 = g.x + static_cast<int>(have * (part + 1) / split);
@@ -334,7 +336,7 @@ cudaError_t column_sums(const void* dy, long long ld, const int32_t* offsets, in
   const int blocks = (n + 127) / 128;
   int split = 1;
   while (split < 8 && static_cast<long long>(blocks) * groups * split < 4LL * device_sm_count()) split *= 2;
-  return launch_kernel(column_sum_kernel<T>, dim3(blocks * split, groups), dim3(256), 0, s, false,
+  return launch_kernel(column_sum_kernel<T>, dim3(blocks * split, groups), dim3(256), 0, s, true,
                        static_cast<unsigned>(split), static_cast<const T*>(dy), ld, offsets, rows, n, out,
                        static_cast<int>(vec));
 }
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const T* dy, long lon
                                                            long long ldd, int rows, int n, int act, int vec) {
   const int quads = (n + 3) / 4;
   const long long total = static_cast<long long>(rows) * quads;
+  pdl_wait();
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += gridDim.x * 256LL) {
     const long long r = i / quads;
     const int c = static_cast<int>(i - r * quads) * 4;
@@ -368,10 +371,10 @@ cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const 
   const long long quads = static_cast<long long>(rows) * ((n + 3) / 4);
   const unsigned grid = static_cast<unsigned>(std::min<long long>((quads + 255) / 256, device_sm_count() * 16LL));
   if (dtype == MOE_DTYPE_F32)
-    return launch_kernel(act_backward_kernel<float>, dim3(grid), dim3(256), 0, s, false, 1, static_cast<const float*>(dy),
+    return launch_kernel(act_backward_kernel<float>, dim3(grid), dim3(256), 0, s, true, 1, static_cast<const float*>(dy),
                          ldy, static_cast<const float*>(z), ldz, static_cast<float*>(dz), ldd, rows, n, act,
                          static_cast<int>(vec));
-  return launch_kernel(act_backward_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, false, 1,
+  return launch_kernel(act_backward_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, true, 1,
                        static_cast<const __nv_bfloat16*>(dy), ldy, static_cast<const __nv_bfloat16*>(z), ldz,
                        static_cast<__nv_bfloat16*>(dz), ldd, rows, n, act, static_cast<int>(vec));
 }

@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_b);
     if (a.tma_store) tma_prefetch_desc(&tm_d);
   }
+  pdl_wait();  // everything before this runs beside the end of the stream's previous kernel
   if (warp == 0) {
     if constexpr (S::kWeight) {
       bool bad = false;
@@ -747,7 +748,7 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUt
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, s, false,
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, s, true,
                        static_cast<unsigned>(cluster), ta, tb, td, tp, t);
 }
 
@@ -782,7 +783,8 @@ double expected_tiles(const Problem& q, int tile) {
 //   kSingle  413, 441   341, 379   265, 318   221, 319
 // (narrow tiles are bound by the issue of loads and MMAs, wide ones by the
 // tensor pipe at the clock that the power limit leaves). A tile costs about
-// 500 more, a pair's start 2000, a split's exchange 1500.
+// 500 more, a pair's start 2000, a split's exchange 1500 a CTA (clusters of 8
+// measured 25 us slower than their share: few fit beside one another).
 Choice choose_tiles(const Problem& q, int sms) {
   Choice best{Form::kSingle, kBN, 1};
   double least = 1e300;
@@ -801,9 +803,9 @@ Choice choose_tiles(const Problem& q, int sms) {
     const double single = (q.weight ? 210 : 165) + 0.9 * bn;
     consider(Form::kPair, bn, 1, expected_tiles(q, 256) * n_tiles, sms / 2, pair, 2000);
     consider(Form::kSingle, bn, 1, expected_tiles(q, 128) * n_tiles, sms, single, 0);
-    for (int split = 2; split <= 8; split *= 2)
+    for (int split = 2; split <= 4; split *= 2)
       if (most_tiles(q, 128) * n_tiles * split <= sms && q.blocks >= 2 * split)
-        consider(Form::kSplit, bn, split, 1, 1, single, 1500);
+        consider(Form::kSplit, bn, split, 1, 1, single, 1500 * split);
   }
   return best;
 }

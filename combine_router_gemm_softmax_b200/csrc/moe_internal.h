@@ -172,7 +172,6 @@ struct DropoutArgs {
 // dropout.cu
 cudaError_t launch_dropout(int dtype, int rows, int cols, const void* x, long long ldx, const void* residual,
                            long long ldr, void* y, long long ldy, const DropoutArgs& d, cudaStream_t s);
-// dispatch.cu
 cudaError_t launch_combine_dropout(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate,
                                    const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
                                    cudaStream_t s);
@@ -197,6 +196,9 @@ struct MatmulArgs {
 };
 // matmul_simt.cu
 cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+// matmul_rows.cu: the forward for few rows a group, and whether a call is that (same demands as matmul_tc.cu)
+bool matmul_few_rows(const MatmulArgs& a);
+cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s);
 // matmul_tc.cu (strides and addresses on 16 bytes)
 cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
 // matmul_simt.cu

@@ -229,7 +229,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
 
 def test_binding_refuses_strides_and_shapes():
     from combine_router_gemm_softmax_b200 import _lib
-    cpu = torch.device("cpu")
+    cpu = -1  # the device index of CPU tensors
     t = torch.zeros(6, 8)
     assert _lib._strided(t, (6, 8), torch.float32, cpu, "t")[1] == 8
     assert _lib._strided(torch.zeros(6, 12)[:, :8], (6, 8), torch.float32, cpu, "t")[1] == 12
