@@ -88,7 +88,7 @@ int forward(const moe_gemm_config* cfg, bool dense, const void* x, const int32_t
   a.n = c.n, a.k = c.k, a.lda = c.ldx, a.ldb = c.ldw, a.b_stride = c.w_stride, a.ldd = c.ldy;
   a.bias = bias, a.preact = preact, a.residual = residual, a.ldz = c.ldz, a.ldr = c.ldr;
   a.d = y, a.act = c.act, a.status = status;
-  a.vec_a = c.ldx % 4 == 0, a.vec_b = c.ldw % 4 == 0 && c.w_stride % 4 == 0;
+  a.vec = c.k % 4 == 0 && c.ldx % 4 == 0 && c.ldw % 4 == 0 && c.w_stride % 4 == 0;
   return rc_of(launch_product(c.dtype, MatmulMode::kForward, a, s));
 }
 
@@ -107,7 +107,7 @@ int dgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
   a.n = c.k, a.k = c.n, a.lda = c.ldy, a.ldb = c.ldw, a.b_stride = c.w_stride, a.ldd = c.ldx;
   a.z = z, a.residual = residual, a.ldz = c.ldz, a.ldr = c.ldr;
   a.d = dx, a.act = c.act, a.status = status;
-  a.vec_a = c.ldy % 4 == 0, a.vec_b = c.ldw % 4 == 0 && c.w_stride % 4 == 0;
+  a.vec = c.n % 4 == 0 && c.k % 4 == 0 && c.ldy % 4 == 0 && c.ldw % 4 == 0 && c.w_stride % 4 == 0;
   return rc_of(launch_product(c.dtype, MatmulMode::kDgrad, a, s));
 }
 
@@ -132,12 +132,12 @@ int wgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
     a.a = dy, a.b = x, a.offsets = offsets, a.groups = c.groups, a.rows = c.rows;
     a.m = c.n, a.n = c.k, a.lda = c.ldy, a.ldb = c.ldx, a.ldd = c.k;
     a.d = dw, a.status = status;
-    a.vec_a = c.ldy % 4 == 0, a.vec_b = c.ldx % 4 == 0;
+    a.vec = c.n % 4 == 0 && c.k % 4 == 0 && c.ldy % 4 == 0 && c.ldx % 4 == 0;
     const int rc = rc_of(launch_product(c.dtype, MatmulMode::kWgrad, a, s));
     if (rc != MOE_OK) return rc;
   }
   if (dbias)
-    return rc_of(launch_column_sums(c.dtype, dy, c.ldy, offsets, c.groups, c.rows, c.n, dbias, c.ldy % 4 == 0, s));
+    return rc_of(launch_column_sums(c.dtype, dy, c.ldy, offsets, c.groups, c.rows, c.n, dbias, c.n % 4 == 0 && c.ldy % 4 == 0, s));
   return MOE_OK;
 }
 
@@ -197,7 +197,7 @@ int32_t moe_act_backward(const moe_gemm_config* cfg, const void* dy, const void*
   if (c.rows > 0 && (!dy || !z || !dz)) return MOE_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16)) return MOE_ERR_UNSUPPORTED;
   if (c.rows == 0) return MOE_OK;
-  const bool vec = c.ldy % 4 == 0 && c.ldz % 4 == 0;
+  const bool vec = c.n % 4 == 0 && c.ldy % 4 == 0 && c.ldz % 4 == 0 && c.ldr % 4 == 0;
   return rc_of(launch_act_backward(c.dtype, dy, c.ldy, z, c.ldz, dz, c.ldr, c.rows, c.n, c.act, vec,
                                    static_cast<cudaStream_t>(stream)));
 }

@@ -25,7 +25,7 @@ MOE_DEV int2 group_rows(const int32_t* offsets, int e, int rows, bool* bad = nul
   return make_int2(r0, r1);
 }
 
-// One warp: s_rows[e] = group e's rows, prefix[e] = row tiles (of 2^tile_shift rows)
+// One warp: s_rows[e] (if wanted) = group e's rows, prefix[e] = row tiles (of 2^tile_shift rows)
 // before group e, prefix[E] = all of them. E <= kMaxE (eight groups a lane).
 MOE_DEV void build_groups(const int32_t* offsets, int E, int rows, int tile_shift, int2* s_rows, int* prefix,
                           int32_t* status, int lane) {
@@ -38,7 +38,7 @@ MOE_DEV void build_groups(const int32_t* offsets, int E, int rows, int tile_shif
     loc[v] = 0;
     if (e < E) {
       const int2 r = group_rows(offsets, e, rows, &bad);
-      s_rows[e] = r;
+      if (s_rows != nullptr) s_rows[e] = r;
       loc[v] = (r.y - r.x + (1 << tile_shift) - 1) >> tile_shift;
     }
     sum += loc[v];
@@ -74,45 +74,77 @@ MOE_DEV int group_of_tile(const int* prefix, int E, int t) {
 }
 
 // ------------------------------------------------------------------ activations
-// Phi, the standard normal distribution function, by Abramowitz and Stegun
-// 7.1.26: erfc(t) = p(s) exp(-t^2), s = 1 / (1 + 0.3275911 t), absolute error
-// at most 1.5e-7, and gauss = exp(-z^2 / 2). For results that are rounded to
-// bf16 next.
-MOE_DEV float phi_fast(float z, float& gauss) {
-  const float t = fabsf(z) * 0.70710678f;
-  const float s = __fdividef(1.0f, fmaf(0.3275911f, t, 1.0f));
-  gauss = __expf(-t * t);
-  float p = fmaf(1.061405429f, s, -1.453152027f);
-  p = fmaf(p, s, 1.421413741f);
-  p = fmaf(p, s, -0.284496736f);
-  p = fmaf(p, s, 0.254829592f);
-  const float tail = 0.5f * p * s * gauss;  // Phi(-|z|)
-  return z < 0.0f ? tail : 1.0f - tail;
+// Two forms of each: for fp32 outputs the IEEE functions, for outputs that are
+// rounded to bf16 (kFast) base-2 exponentials and reciprocals by the
+// approximate instructions (about 2 ulp) with the constants folded, since the
+// activation's issue slots are what bounds an epilogue of a short reduction:
+// the slope of GELU's tanh form takes 11 instructions instead of 25.
+MOE_DEV float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// kFast: the fast exponential, reciprocal and phi_fast (about 1e-6 relative,
-// or absolute in Phi), for outputs rounded to bf16; else the IEEE forms, for
-// fp32 outputs.
+MOE_DEV float rcp_fast(float x) {  // 0 for infinity
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kGeluTanhC = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluTanhA = 0.044715f;
+
+// 1 / (1 + e^-z)
 template <bool kFast>
 MOE_DEV float sigmoid_of(float z) {
-  // __fdividef returns 0 for divisors above 2^126 (z < -87): below every bf16 product of interest
-  return kFast ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
+  return kFast ? rcp_fast(1.0f + ex2_fast(-kLog2E * z)) : 1.0f / (1.0f + expf(-z));
 }
 
-constexpr float kGeluTanhC = 0.7978845608028654f;  // sqrt(2 / pi)
+// sigmoid(2 u) with u = sqrt(2/pi) (z + 0.044715 z^3). The tanh form of GELU is
+// z sigmoid(2 u), since (1 + tanh u) / 2 = sigmoid(2 u): no cancellation for
+// negative z.
+template <bool kFast>
+MOE_DEV float gelu_sigmoid(float z) {
+  if constexpr (kFast) {
+    const float p = fmaf(z * z, -2.0f * kLog2E * kGeluTanhC * kGeluTanhA, -2.0f * kLog2E * kGeluTanhC);
+    return rcp_fast(1.0f + ex2_fast(z * p));
+  } else {
+    return sigmoid_of<false>(2.0f * kGeluTanhC * (z + kGeluTanhA * z * z * z));
+  }
+}
 
-// The tanh form of GELU is z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3),
-// since (1 + tanh u) / 2 = sigmoid(2 u): no cancellation for negative z.
+// Phi, the standard normal distribution function, and gauss = exp(-z^2 / 2).
+// Fast: Abramowitz and Stegun 7.1.26, erfc(t) = p(s) exp(-t^2) with
+// s = 1 / (1 + 0.3275911 t), absolute error at most 1.5e-7 (coefficients
+// halved: Phi(-|z|) = erfc(|z| / sqrt(2)) / 2). Else erfc itself, which keeps
+// its relative precision in the negative tail.
+template <bool kFast>
+MOE_DEV float phi_of(float z, float& gauss) {
+  if constexpr (kFast) {
+    const float s = rcp_fast(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+    gauss = ex2_fast(z * z * (-0.5f * kLog2E));
+    float p = fmaf(0.5f * 1.061405429f, s, -0.5f * 1.453152027f);
+    p = fmaf(p, s, 0.5f * 1.421413741f);
+    p = fmaf(p, s, -0.5f * 0.284496736f);
+    p = fmaf(p, s, 0.5f * 0.254829592f);
+    const float tail = p * s * gauss;  // Phi(-|z|)
+    return z < 0.0f ? tail : 1.0f - tail;
+  } else {
+    gauss = expf(-0.5f * z * z);
+    return 0.5f * erfcf(-z * 0.70710678118654752f);
+  }
+}
+
 template <int kAct, bool kFast>
 MOE_DEV float act_value(float z) {
   if constexpr (kAct == MOE_ACT_RELU) {
     return z > 0.0f ? z : (z != z ? z : 0.0f);
   } else if constexpr (kAct == MOE_ACT_GELU) {
     float gauss;
-    // erfc keeps its relative precision in the negative tail
-    return z * (kFast ? phi_fast(z, gauss) : 0.5f * erfcf(-z * 0.70710678118654752f));
+    return z * phi_of<kFast>(z, gauss);
   } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
-    return z * sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
+    return z * gelu_sigmoid<kFast>(z);
   } else if constexpr (kAct == MOE_ACT_SILU) {
     return z * sigmoid_of<kFast>(z);
   } else {
@@ -125,21 +157,16 @@ MOE_DEV float slope_value(float z) {
   if constexpr (kAct == MOE_ACT_RELU) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (kAct == MOE_ACT_GELU) {
-    float gauss, phi;
-    if constexpr (kFast) {
-      phi = phi_fast(z, gauss);
-    } else {
-      phi = 0.5f * erfcf(-z * 0.70710678118654752f);
-      gauss = expf(-0.5f * z * z);
-    }
+    float gauss;
+    const float phi = phi_of<kFast>(z, gauss);
     return fmaf(z * 0.3989422804014327f, gauss, phi);
   } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
-    const float s = sigmoid_of<kFast>(2.0f * kGeluTanhC * (z + 0.044715f * z * z * z));
-    const float du = 2.0f * kGeluTanhC * (1.0f + 3.0f * 0.044715f * z * z);
-    return fmaf(z * s * (1.0f - s), du, s);
+    const float s = gelu_sigmoid<kFast>(z);
+    const float du = fmaf(z * z, 6.0f * kGeluTanhC * kGeluTanhA, 2.0f * kGeluTanhC);
+    return fmaf(z * fmaf(-s, s, s), du, s);
   } else if constexpr (kAct == MOE_ACT_SILU) {
     const float s = sigmoid_of<kFast>(z);
-    return s * fmaf(z, 1.0f - s, 1.0f);
+    return fmaf(z, fmaf(-s, s, s), s);
   } else {
     return 1.0f;
   }

@@ -27,45 +27,50 @@ struct Quad {
 };
 
 // Four elements from p, `valid` of them inside the row (the others zero).
-template <typename T>
-MOE_DEV Quad load4(const T* p, int valid, bool vec) {
-  Quad q;
-  if (valid >= 4 && vec) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p);
-      q.v[0] = f.x, q.v[1] = f.y, q.v[2] = f.z, q.v[3] = f.w;
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-      const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-      q.v[0] = lo.x, q.v[1] = lo.y, q.v[2] = hi.x, q.v[3] = hi.y;
+// kVec: the row's width is a multiple of four and it starts on four elements'
+// alignment, so that all four exist or none; one load under one predicate.
+template <typename T, bool kVec>
+MOE_DEV Quad load4(const T* p, int valid) {
+  Quad q{};
+  if constexpr (kVec) {
+    if (valid > 0) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        q.v[0] = f.x, q.v[1] = f.y, q.v[2] = f.z, q.v[3] = f.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+        const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+        q.v[0] = lo.x, q.v[1] = lo.y, q.v[2] = hi.x, q.v[3] = hi.y;
+      }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q.v[j] = j < valid ? to_f32(p[j]) : 0.0f;
+    for (int j = 0; j < 4; ++j)
+      if (j < valid) q.v[j] = to_f32(p[j]);
   }
   return q;
 }
 
 // One operand's slice of BT (rows of the tile) x 16 (reduction), in registers.
 // kAlong: elements lie along the reduction (row-major tile rows); else across.
-template <bool kAlong, int BT>
+template <bool kAlong, bool kVec, int BT>
 struct Slice {
   static constexpr int kQuads = BT * kBK / 4 / kThreads;
   Quad q[kQuads];
 
   // base: element (first row of the tile, reduction index 0); rows and
   // depth: what of the tile and of the reduction [k0, ...) exists.
-  MOE_DEV void load(const float* base, long long ld, int rows, int k0, int depth, bool vec) {
+  MOE_DEV void load(const float* base, long long ld, int rows, int k0, int depth) {
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
       const int id = threadIdx.x + i * kThreads;
       if constexpr (kAlong) {
         const int r = id >> 2, k = k0 + (id & 3) * 4;
-        q[i] = load4(base + r * ld + k, r < rows ? depth - k : 0, vec);
+        q[i] = load4<float, kVec>(base + r * ld + k, r < rows ? depth - k : 0);
       } else {
         const int k = k0 + id / (BT / 4), r = (id % (BT / 4)) * 4;
-        q[i] = load4(base + k * ld + r, k < depth ? rows - r : 0, vec);
+        q[i] = load4<float, kVec>(base + k * ld + r, k < depth ? rows - r : 0);
       }
     }
   }
@@ -109,7 +114,7 @@ MOE_DEV int at(int t, int i) {
   return BT == 128 ? (i >> 2) * 64 + t * 4 + (i & 3) : t * 4 + i;
 }
 
-template <MatmulMode kMode, int BT>
+template <MatmulMode kMode, bool kVec, int BT>
 __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs a) {
   constexpr int kPer = BT / 16;  // outputs of a thread along each axis
   constexpr bool kWeight = kMode == MatmulMode::kWgrad;
@@ -166,11 +171,11 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
 #pragma unroll
       for (int j = 0; j < kPer / 2; ++j) acc[i][j] = 0;
 
-    Slice<!kWeight, BT> qa;
-    Slice<kMode == MatmulMode::kForward, BT> qb;
+    Slice<!kWeight, kVec, BT> qa;
+    Slice<kMode == MatmulMode::kForward, kVec, BT> qb;
     if (k_first < depth) {
-      qa.load(pa, a.lda, m_valid, k_first, depth, a.vec_a);
-      qb.load(pb, a.ldb, n_valid, k_first, depth, a.vec_b);
+      qa.load(pa, a.lda, m_valid, k_first, depth);
+      qb.load(pb, a.ldb, n_valid, k_first, depth);
       qa.store(sA[0]);
       qb.store(sB[0]);
     }
@@ -179,8 +184,8 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
     for (int k0 = k_first; k0 < depth; k0 += kBK, buf ^= 1) {
       const bool more = k0 + kBK < depth;
       if (more) {
-        qa.load(pa, a.lda, m_valid, k0 + kBK, depth, a.vec_a);
-        qb.load(pb, a.ldb, n_valid, k0 + kBK, depth, a.vec_b);
+        qa.load(pa, a.lda, m_valid, k0 + kBK, depth);
+        qb.load(pb, a.ldb, n_valid, k0 + kBK, depth);
       }
 #pragma unroll
       for (int k = 0; k < kBK; ++k) {
@@ -250,8 +255,8 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
   }
 }
 
-template <MatmulMode kMode>
-cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
+template <MatmulMode kMode, bool kVec>
+cudaError_t launch_tiles(const MatmulArgs& a, cudaStream_t s) {
   const int sms = device_sm_count();
   // no more than these row tiles exist, however the rows fall to the groups
   auto tiles = [&](long long bt) {
@@ -261,15 +266,20 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
     return tm * tn;
   };
   if (tiles(128) >= sms)
-    return launch_kernel(matmul_simt_kernel<kMode, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
+    return launch_kernel(matmul_simt_kernel<kMode, kVec, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
                          dim3(kThreads), 0, s, true, 1, a);
   const long long t = tiles(64);
   const int depth = kMode == MatmulMode::kWgrad ? a.rows : a.k;
   int split = 1;
   while (split < 8 && t * split * 2 <= 2 * sms && depth / (split * 2) >= 64) split *= 2;
   const long long grid = std::min<long long>(t, 4 * sms) * split;
-  return launch_kernel(matmul_simt_kernel<kMode, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, true,
+  return launch_kernel(matmul_simt_kernel<kMode, kVec, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, true,
                        static_cast<unsigned>(split), a);
+}
+
+template <MatmulMode kMode>
+cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
+  return a.vec ? launch_tiles<kMode, true>(a, s) : launch_tiles<kMode, false>(a, s);
 }
 
 }  // namespace
@@ -286,16 +296,18 @@ cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t
 }
 
 // ------------------------------------------------------------------ bias gradient
-// db[e, n] = sum of dy[r, n] over group e's rows. A CTA of 256 threads takes
-// 8 warps x 32 lanes of four columns each; the cluster's CTAs share the rows,
-// and their sums meet in distributed shared memory in rank order.
-// Bound: HBM (dy read once).
+// db[e, n] = sum of dy[r, n] over group e's rows. A CTA's 16 warps take 128
+// columns (four a lane) and every 16th row, 16 rows in flight each; the
+// cluster's CTAs share the rows, and their sums meet in distributed shared
+// memory in rank order. Bound: HBM (dy read once).
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(256) column_sum_kernel(const T* dy, long long ld, const int32_t* offsets, int rows,
-                                                         int n, float* out, int vec) {
-  __shared__ __align__(16) float s_sum[8][128];
+constexpr int kSumWarps = 16, kSumRows = 16;
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const T* dy, long long ld, const int32_t* offsets,
+                                                                    int rows, int n, float* out) {
+  __shared__ __align__(16) float s_sum[kSumWarps][128];
   uint32_t split, part;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
   part = split > 1 ? cluster_ctarank() : 0;
@@ -306,25 +318,30 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const T* dy, long long 
   const long long have = g.y - g.x;
   const int r0 = g.x + static_cast<int>(have * part / split), r1 = g.x + static_cast<int>(have * (part + 1) / split);
   const int c = n0 + lane * 4;
+  const T* p = dy + c;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int r = r0 + warp; r < r1; r += 8) {
-    const Quad q = load4(dy + static_cast<long long>(r) * ld + c, n - c, vec != 0);
+  for (int r = r0 + warp; r < r1; r += kSumRows * kSumWarps) {
+    Quad q[kSumRows];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] += q.v[j];
+    for (int i = 0; i < kSumRows; ++i)
+      q[i] = load4<T, kVec>(p + static_cast<long long>(r + i * kSumWarps) * ld, r + i * kSumWarps < r1 ? n - c : 0);
+#pragma unroll
+    for (int i = 0; i < kSumRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += q[i].v[j];
   }
   *reinterpret_cast<float4*>(&s_sum[warp][lane * 4]) = make_float4(s[0], s[1], s[2], s[3]);
   __syncthreads();
   if (threadIdx.x < 128) {
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += s_sum[w][threadIdx.x];
+    for (int w = 0; w < kSumWarps; ++w) t += s_sum[w][threadIdx.x];
     s_sum[0][threadIdx.x] = t;
   }
   if (split > 1) cluster_sync();
   if (part == 0 && threadIdx.x < 128 && n0 + static_cast<int>(threadIdx.x) < n) {
     float t = s_sum[0][threadIdx.x];
-    for (uint32_t p = 1; p < split; ++p) t += ld_shared_cluster_f32(mapa_shared(smem_addr(&s_sum[0][threadIdx.x]), p));
+    for (uint32_t k = 1; k < split; ++k) t += ld_shared_cluster_f32(mapa_shared(smem_addr(&s_sum[0][threadIdx.x]), k));
     out[static_cast<size_t>(e) * n + n0 + threadIdx.x] = t;
   }
   if (split > 1) cluster_sync();
@@ -335,27 +352,52 @@ cudaError_t column_sums(const void* dy, long long ld, const int32_t* offsets, in
                         bool vec, cudaStream_t s) {
   const int blocks = (n + 127) / 128;
   int split = 1;
-  while (split < 8 && static_cast<long long>(blocks) * groups * split < 4LL * device_sm_count()) split *= 2;
-  return launch_kernel(column_sum_kernel<T>, dim3(blocks * split, groups), dim3(256), 0, s, true,
-                       static_cast<unsigned>(split), static_cast<const T*>(dy), ld, offsets, rows, n, out,
-                       static_cast<int>(vec));
+  while (split < 8 && static_cast<long long>(blocks) * groups * split < 2LL * device_sm_count() &&
+         rows / groups / split > kSumRows * kSumWarps)
+    split *= 2;
+  return launch_kernel(vec ? column_sum_kernel<T, true> : column_sum_kernel<T, false>, dim3(blocks * split, groups),
+                       dim3(32 * kSumWarps), 0, s, true, static_cast<unsigned>(split), static_cast<const T*>(dy), ld,
+                       offsets, rows, n, out);
 }
 
-// dz = dy act'(z), elementwise over [rows, n]. Bound: HBM.
-template <typename T>
+// dz = dy act'(z), elementwise over [rows, n], four columns a step. Bound: HBM.
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) act_backward_kernel(const T* dy, long long ldy, const T* z, long long ldz, T* dz,
-                                                           long long ldd, int rows, int n, int act, int vec) {
-  const int quads = (n + 3) / 4;
+                                                           long long ldd, int rows, int n, int act) {
+  const unsigned quads = (n + 3) / 4;
   const long long total = static_cast<long long>(rows) * quads;
   pdl_wait();
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += gridDim.x * 256LL) {
     const long long r = i / quads;
     const int c = static_cast<int>(i - r * quads) * 4;
-    const Quad q = load4(dy + r * ldy + c, n - c, vec != 0), w = load4(z + r * ldz + c, n - c, vec != 0);
+    const Quad q = load4<T, kVec>(dy + r * ldy + c, n - c), w = load4<T, kVec>(z + r * ldz + c, n - c);
+    T out[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (c + j < n) dz[r * ldd + c + j] = from_f32<T>(q.v[j] * act_slope<sizeof(T) == 2>(w.v[j], act));
+    for (int j = 0; j < 4; ++j) out[j] = from_f32<T>(q.v[j] * act_slope<sizeof(T) == 2>(w.v[j], act));
+    T* p = dz + r * ldd + c;
+    if constexpr (kVec) {
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(out[0], out[1], out[2], out[3]);
+      else
+        *reinterpret_cast<uint2*>(p) = make_uint2(
+            static_cast<uint32_t>(__bfloat16_as_ushort(out[0])) | static_cast<uint32_t>(__bfloat16_as_ushort(out[1])) << 16,
+            static_cast<uint32_t>(__bfloat16_as_ushort(out[2])) | static_cast<uint32_t>(__bfloat16_as_ushort(out[3])) << 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < n) p[j] = out[j];
+    }
   }
+}
+
+template <typename T>
+cudaError_t act_backward(const void* dy, long long ldy, const void* z, long long ldz, void* dz, long long ldd, int rows,
+                         int n, int act, bool vec, cudaStream_t s) {
+  const long long quads = static_cast<long long>(rows) * ((n + 3) / 4);
+  const unsigned grid = static_cast<unsigned>(std::min<long long>((quads + 255) / 256, device_sm_count() * 16LL));
+  return launch_kernel(vec ? act_backward_kernel<T, true> : act_backward_kernel<T, false>, dim3(grid), dim3(256), 0, s,
+                       true, 1, static_cast<const T*>(dy), ldy, static_cast<const T*>(z), ldz, static_cast<T*>(dz), ldd,
+                       rows, n, act);
 }
 
 }  // namespace
@@ -368,15 +410,8 @@ cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const in
 
 cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const void* z, long long ldz, void* dz,
                                 long long ldd, int rows, int n, int act, bool vec, cudaStream_t s) {
-  const long long quads = static_cast<long long>(rows) * ((n + 3) / 4);
-  const unsigned grid = static_cast<unsigned>(std::min<long long>((quads + 255) / 256, device_sm_count() * 16LL));
-  if (dtype == MOE_DTYPE_F32)
-    return launch_kernel(act_backward_kernel<float>, dim3(grid), dim3(256), 0, s, true, 1, static_cast<const float*>(dy),
-                         ldy, static_cast<const float*>(z), ldz, static_cast<float*>(dz), ldd, rows, n, act,
-                         static_cast<int>(vec));
-  return launch_kernel(act_backward_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, true, 1,
-                       static_cast<const __nv_bfloat16*>(dy), ldy, static_cast<const __nv_bfloat16*>(z), ldz,
-                       static_cast<__nv_bfloat16*>(dz), ldd, rows, n, act, static_cast<int>(vec));
+  return dtype == MOE_DTYPE_F32 ? act_backward<float>(dy, ldy, z, ldz, dz, ldd, rows, n, act, vec, s)
+                                : act_backward<__nv_bfloat16>(dy, ldy, z, ldz, dz, ldd, rows, n, act, vec, s);
 }
 
 }  // namespace moe

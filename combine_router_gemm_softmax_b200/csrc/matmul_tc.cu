@@ -16,7 +16,7 @@
 // offsets. Warp 0 loads a ring of up to 8 stages (192 KB) by TMA, one thread
 // of warp 1 issues tcgen05.mma into one of two TMEM accumulators, warps 2..9
 // drain the other: bias, activation, slope and residual in fp32, one rounding,
-// and 32 x 32 blocks through shared memory to TMA stores. Three forms:
+// and 32 x 32 blocks through shared memory to coalesced stores. Three forms:
 //
 //   kPair    256 x bn tiles on a cluster of two CTAs (cta_group::2): each loads
 //            128 rows of A and half of B, 32 KB a stage at bn = 256, so that
@@ -59,20 +59,24 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kChainBlocks = 8;  // wgrad: blocks of the reduction added in one accumulator
 constexpr uint32_t kABytes = kBM * kBK * 2;  // one CTA's rows of A
-constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements
 
 enum class Form { kSingle, kSplit, kPair };
 
+// Blocks of 64 along the reduction that a stage of the ring holds. Two halve
+// the barrier traffic of a block, which bounds narrow tiles (pairs of width
+// 128: 221 -> 187 ns a block); the 48 KB blocks of wide single tiles leave no
+// room for them.
+constexpr int blocks_per_stage(Form f) { return f == Form::kPair ? 2 : 1; }
+
 struct TcArgs {
   MatmulArgs p;
   int bn;                // columns of a tile: a multiple of 32 up to kBN
   int stages;            // of the operand ring
-  uint32_t stage_bytes;  // of one CTA's ring
+  uint32_t block_bytes;  // of one block in one CTA's ring
   int n_tiles, m_tiles;  // column tiles; weight mode: row tiles of one group
   int band;              // row tiles per band of the tile walk
-  int tma_store;         // D (and preact) have store maps
 };
 
 // full, empty, tails and zeroed per stage, two accumulators' full and empty, the drain; even
@@ -83,9 +87,10 @@ struct Shape {
   static constexpr bool kWeight = kMode == MatmulMode::kWgrad;
   static constexpr bool kAcrossA = kWeight;                       // A lies across the reduction
   static constexpr bool kAcrossB = kMode != MatmulMode::kForward;  // B does
-  static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 32 * 64;  // one 32 x 32 block of the output
+  static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 32 * 64;  // a 32 x 32 block of the output, a warp's
+  static constexpr uint32_t kRingBytes = 192 * 1024;
   static constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStgBytes + kBarriers * 8 + 16 +
-                                  (kWeight ? 0 : kEpiWarps * 32 * 4 + kMaxE * 8 + (kMaxE + 1) * 4);
+                                  (kWeight ? 0 : (kMaxE + 1) * 4);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -133,141 +138,161 @@ MOE_DEV void load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int
     tma_load_3d_at(dst, map, bar, x, y, z);
 }
 
-// 32 bf16 of a row from column n0 (n columns in all); columns past n are zero.
-MOE_DEV void load_row(const void* base, long long at, int n0, int n, float (&f)[32]) {
+// 32 bf16 of a row from column n0 (n columns in all), as they are; columns
+// past n, and all of them where the lane has no row, are zero.
+struct Row32 {
+  uint4 q[4];
+};
+
+MOE_DEV Row32 load_row(const void* base, long long at, int n0, int n, bool valid) {
+  Row32 r;
   const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + at;
   if (n0 + 32 <= n) {
-    uint4 q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q[i]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 t = __bfloat1622float2(h[j]);
-        f[8 * i + 2 * j] = t.x;
-        f[8 * i + 2 * j + 1] = t.y;
-      }
-    }
+    for (int i = 0; i < 4; ++i) r.q[i] = valid ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
   } else {
+    uint32_t h[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = n0 + i < n ? __bfloat162float(p[i]) : 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t lo = valid && n0 + 2 * i < n ? __bfloat16_as_ushort(p[2 * i]) : 0;
+      const uint32_t hi = valid && n0 + 2 * i + 1 < n ? __bfloat16_as_ushort(p[2 * i + 1]) : 0;
+      h[i] = lo | (hi << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.q[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
   }
+  return r;
 }
 
-// A lane's row of 32 columns to a bf16 matrix: the whole warp's block by TMA
-// where all 32 rows are the group's (`staged`), else row by row.
-MOE_DEV void store_rows(const float (&f)[32], void* base, long long at, int n0, int n, bool valid, bool staged,
-                        uint8_t* stg, int lane, const CUtensorMap* tm, int row0) {
-  uint32_t q[16];
+MOE_DEV float2 pair_of(const Row32& r, int i) {  // elements 2 i and 2 i + 1
+  const uint4& q = r.q[i >> 2];
+  const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+// A warp's 32 x 32 block of the output, a row a lane in v, to global memory:
+// through shared memory (16-byte chunk j of row r at j ^ (r & 7), or with
+// 64-byte rows at j ^ (r / 2 & 3)), so that a store instruction writes whole
+// rows of the block (4 of 128 bytes, 8 of 64). rows, cols: what of the block
+// exists. TMA stores from the same buffers cost a proxy fence a block, on which
+// the epilogue warps of a short reduction spent most of their time.
+template <typename T>
+MOE_DEV void store_block(uint8_t* stg, const uint4 (&v)[sizeof(T) * 2], T* out, long long ld, int rows, int cols,
+                         bool vec, int lane) {
+  constexpr int kChunks = sizeof(T) * 2, kPer = 16 / sizeof(T);  // chunks of a row, elements of a chunk
+  auto place = [](int r, int j) { return r * kChunks * 16 + ((j ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) q[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-  const uint4 v[4] = {make_uint4(q[0], q[1], q[2], q[3]), make_uint4(q[4], q[5], q[6], q[7]),
-                      make_uint4(q[8], q[9], q[10], q[11]), make_uint4(q[12], q[13], q[14], q[15])};
-  if (staged) {
-    stage_store_rows<64>(stg, v, lane, tm, n0, row0);
-  } else if (valid) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at;
-    if (n0 + 32 <= n) {
+  for (int j = 0; j < kChunks; ++j) *reinterpret_cast<uint4*>(stg + place(lane, j)) = v[j];
+  __syncwarp();
+  const int j = lane % kChunks, have = cols - j * kPer;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+  for (int i = 0; i < kChunks; ++i) {
+    const int r = i * (32 / kChunks) + lane / kChunks;
+    const uint4 q = *reinterpret_cast<const uint4*>(stg + place(r, j));
+    if (r >= rows) continue;
+    T* p = out + r * ld + j * kPer;
+    if (have >= kPer && vec) {
+      *reinterpret_cast<uint4*>(p) = q;
     } else {
+      const T* e = reinterpret_cast<const T*>(&q);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (n0 + i < n) p[i] = __float2bfloat16_rn(f[i]);
+      for (int x = 0; x < kPer; ++x)
+        if (x < have) p[x] = e[x];
     }
   }
 }
 
-// The epilogue of one 32 x 32 block of rows mode: this lane's row r (valid or
-// not), columns n0 .. n0 + 31, sums in f.
+// The same for sums rounded to bf16 here.
+MOE_DEV void store_rows(uint8_t* stg, const float (&f)[32], void* base, long long at, long long ld, int rows, int cols,
+                        int lane) {
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                      pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+  store_block(stg, v, static_cast<__nv_bfloat16*>(base) + at, ld, rows, cols, true, lane);
+}
+
+// What the epilogue of a rows-mode block reads besides the sums, loaded ahead
+// of them: z (dgrad, if any) or else the residual.
 template <bool kDgrad>
-MOE_DEV void finish_rows(const TcArgs& a, float (&f)[32], int e, long long r, int row0, int n0, bool valid, bool staged,
-                         uint8_t* stg, float* s_bias, int lane, const CUtensorMap* tm_d, const CUtensorMap* tm_p) {
-  const MatmulArgs& p = a.p;
-  float g[32];
+MOE_DEV Row32 load_ahead(const MatmulArgs& p, long long r, int n0, bool valid) {
+  if (kDgrad && p.z != nullptr) return load_row(p.z, r * p.ldz + n0, n0, p.n, valid);
+  if (p.residual != nullptr) return load_row(p.residual, r * p.ldr + n0, n0, p.n, valid);
+  return Row32{};
+}
+
+// The epilogue of one 32 x 32 block of rows mode: rows row0 .. of which the
+// group has `left`, this lane's the lane-th; columns n0 ..; sums in f.
+template <bool kDgrad>
+MOE_DEV void finish_rows(const MatmulArgs& p, float (&f)[32], const Row32& ahead, int e, long long row0, int left, int n0,
+                         uint8_t* stg, int lane) {
   if constexpr (kDgrad) {
-    if (p.z != nullptr && valid) {
-      load_row(p.z, r * p.ldz + n0, n0, p.n, g);
+    if (p.z != nullptr) {
       with_act(p.act, [&](auto k) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] *= slope_value<decltype(k)::value, true>(g[i]);
+        for (int i = 0; i < 16; ++i) {
+          const float2 z = pair_of(ahead, i);
+          f[2 * i] *= slope_value<decltype(k)::value, true>(z.x);
+          f[2 * i + 1] *= slope_value<decltype(k)::value, true>(z.y);
+        }
       });
     }
   } else {
     if (p.bias != nullptr) {
-      __syncwarp();
-      s_bias[lane] = n0 + lane < p.n ? p.bias[static_cast<size_t>(e) * p.n + n0 + lane] : 0.0f;
-      __syncwarp();
+      const float b = n0 + lane < p.n ? p.bias[static_cast<size_t>(e) * p.n + n0 + lane] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 b = *reinterpret_cast<const float4*>(s_bias + 4 * i);
-        f[4 * i] += b.x, f[4 * i + 1] += b.y, f[4 * i + 2] += b.z, f[4 * i + 3] += b.w;
-      }
+      for (int i = 0; i < 32; ++i) f[i] += __shfl_sync(0xffffffffu, b, i);
     }
-    if (p.preact != nullptr) store_rows(f, p.preact, r * p.ldz + n0, n0, p.n, valid, staged, stg, lane, tm_p, row0);
+    if (p.preact != nullptr) store_rows(stg, f, p.preact, row0 * p.ldz + n0, p.ldz, left, p.n - n0, lane);
     if (p.act != MOE_ACT_NONE)
       with_act(p.act, [&](auto k) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] = act_value<decltype(k)::value, true>(f[i]);
       });
   }
-  if (p.residual != nullptr && valid) {
-    load_row(p.residual, r * p.ldr + n0, n0, p.n, g);
+  if (p.residual != nullptr) {
+    const Row32 res = kDgrad && p.z != nullptr
+                          ? load_row(p.residual, (row0 + lane) * p.ldr + n0, n0, p.n, lane < left)
+                          : ahead;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] += g[i];
+    for (int i = 0; i < 16; ++i) {
+      const float2 t = pair_of(res, i);
+      f[2 * i] += t.x;
+      f[2 * i + 1] += t.y;
+    }
   }
-  store_rows(f, p.d, r * p.ldd + n0, n0, p.n, valid, staged, stg, lane, tm_d, row0);
+  store_rows(stg, f, p.d, row0 * p.ldd + n0, p.ldd, left, p.n - n0, lane);
 }
 
-// The same for wgrad: row m of group e's fp32 gradient.
-MOE_DEV void finish_weight(const TcArgs& a, const float (&f)[32], int e, int m, int row0, int n0, uint8_t* stg, int lane,
-                           const CUtensorMap* tm_d) {
-  const MatmulArgs& p = a.p;
-  if (a.tma_store) {  // the map ends at the gradient's last row and column
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
+// One 32 x 32 block to its epilogue (weight mode: fp32 rows of group e's gradient).
+template <MatmulMode kMode>
+MOE_DEV void finish_block(const MatmulArgs& p, float (&f)[32], const Row32& ahead, const Tile& c, int row0, int left,
+                          int n0, uint8_t* stg, int lane) {
+  if constexpr (Shape<kMode>::kWeight) {
+    uint4 v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-          make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_3d(tm_d, stg, n0, row0, e);
-      bulk_commit();
-    }
-  } else if (m < p.m) {
-    float* d = static_cast<float*>(p.d) + (static_cast<long long>(e) * p.m + m) * p.ldd + n0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (n0 + i < p.n) d[i] = f[i];
+      v[j] = make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
+                        __float_as_uint(f[4 * j + 3]));
+    store_block(stg, v, static_cast<float*>(p.d) + (static_cast<long long>(c.e) * p.m + row0) * p.ldd + n0, p.ldd, left,
+                p.n - n0, p.ldd % 4 == 0, lane);
+  } else {
+    finish_rows<kMode == MatmulMode::kDgrad>(p, f, ahead, c.e, row0, left, n0, stg, lane);
   }
-}
-
-// One rows-mode or weight-mode block of 32 x 32 to its epilogue.
-template <MatmulMode kMode>
-MOE_DEV void finish_block(const TcArgs& a, float (&f)[32], const Tile& c, int row0, int left, int n0, uint8_t* stg,
-                          float* s_bias, int lane, const CUtensorMap* tm_d, const CUtensorMap* tm_p) {
-  if constexpr (Shape<kMode>::kWeight)
-    finish_weight(a, f, c.e, row0 + lane, row0, n0, stg, lane, tm_d);
-  else
-    finish_rows<kMode == MatmulMode::kDgrad>(a, f, c.e, row0 + lane, row0, n0, lane < left, a.tma_store && left >= 32,
-                                             stg, s_bias, lane, tm_d, tm_p);
 }
 
 template <MatmulMode kMode, Form kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_p,
                      const TcArgs a) {
   using S = Shape<kMode>;
   constexpr bool kPair = kForm == Form::kPair, kSplit = kForm == Form::kSplit;
-  constexpr int kTileM = kPair ? 2 * kBM : kBM;
+  constexpr int kTileM = kPair ? 2 * kBM : kBM, kPerStage = blocks_per_stage(kForm);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);  // the ring: per stage A, then B
-  uint8_t* stg_all = smem + kRingBytes;
+  uint8_t* stg_all = smem + S::kRingBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * S::kStgBytes);
   uint64_t* empty = full + kMaxStages;
   // kPair, weight mode, a block with rows to zero: the second CTA's loads
@@ -280,10 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + kBarriers);  // 16-byte aligned, and what follows it
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* consumed_slot = reinterpret_cast<int*>(tmem_slot + 2);
-  // rows modes only
-  float* s_bias = reinterpret_cast<float*>(tmem_slot + 4);
-  int2* s_rows = reinterpret_cast<int2*>(s_bias + kEpiWarps * 32);
-  int* prefix = reinterpret_cast<int*>(s_rows + kMaxE);
+  int* prefix = reinterpret_cast<int*>(tmem_slot + 4);  // rows modes: row tiles before each group
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const MatmulArgs& p = a.p;
@@ -315,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
-    if (a.tma_store) tma_prefetch_desc(&tm_d);
   }
   pdl_wait();  // everything before this runs beside the end of the stream's previous kernel
   if (warp == 0) {
@@ -324,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = lane; e < p.groups; e += 32) group_rows(p.offsets, e, p.rows, &bad);
       if (bad && blockIdx.x == 0) report_status(p.status, MOE_STATUS_BAD_OFFSETS);
     } else {
-      build_groups(p.offsets, p.groups, p.rows, kPair ? 8 : 7, s_rows, prefix, p.status, lane);
+      build_groups(p.offsets, p.groups, p.rows, kPair ? 8 : 7, nullptr, prefix, p.status, lane);
     }
   } else if (warp == 1) {
     if constexpr (kPair) {
@@ -341,34 +362,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int m_total = S::kWeight ? p.groups * a.m_tiles : prefix[p.groups];
-  const long long total = static_cast<long long>(m_total) * a.n_tiles;
-  const long long first_tile = blockIdx.x / split;
-  const long long step = kSplit ? (1LL << 62) : gridDim.x / split;  // a split cluster has one tile (or none)
+  const uint32_t total = static_cast<uint32_t>(m_total) * a.n_tiles;  // below 2^31 (launch_mode)
+  const uint32_t first_tile = blockIdx.x / split;
+  const uint32_t step = kSplit ? 1u << 31 : gridDim.x / split;  // a split cluster has one tile (or none)
 
   // Bands of row tiles, each swept over all column tiles, so that a wave of
   // CTAs shares A and B in L2; in weight mode the bands stay inside a group.
-  auto tile_at = [&](long long t) {
+  auto tile_at = [&](uint32_t t) {
     Tile c;
     if constexpr (S::kWeight) {
-      const int per = a.m_tiles * a.n_tiles;
-      c.e = static_cast<int>(t / per);
-      const int rem = static_cast<int>(t - static_cast<long long>(c.e) * per);
-      const int b = rem / (a.band * a.n_tiles), within = rem - b * a.band * a.n_tiles;
-      const int rows = min(a.band, a.m_tiles - b * a.band);
+      const uint32_t per = a.m_tiles * a.n_tiles, band_tiles = a.band * a.n_tiles;
+      c.e = t / per;
+      const uint32_t rem = t - c.e * per, b = rem / band_tiles, within = rem - b * band_tiles;
+      const uint32_t rows = min(a.band, static_cast<int>(a.m_tiles - b * a.band));
       c.m = b * a.band + within % rows;
       c.n = within / rows;
       c.rows = group_rows(p.offsets, c.e, p.rows);
       c.kb0 = 0;
       c.kb1 = (c.rows.y - c.rows.x + kBK - 1) / kBK;
     } else {
-      const long long band_tiles = static_cast<long long>(a.band) * a.n_tiles;
-      const int b = static_cast<int>(t / band_tiles), within = static_cast<int>(t - b * band_tiles);
-      const int rows = min(a.band, m_total - b * a.band);
+      const uint32_t band_tiles = a.band * a.n_tiles, b = t / band_tiles, within = t - b * band_tiles;
+      const uint32_t rows = min(a.band, static_cast<int>(m_total - b * a.band));
       const int gm = b * a.band + within % rows;
       c.n = within / rows;
       c.e = group_of_tile(prefix, p.groups, gm);
       c.m = gm - prefix[c.e];
-      c.rows = s_rows[c.e];
+      c.rows = group_rows(p.offsets, c.e, p.rows);
       c.kb0 = 0;
       c.kb1 = (p.k + kBK - 1) / kBK;
     }
@@ -385,8 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kUnit = kPair ? 32 : 16;
     return min(a.bn, (p.n - c.n * a.bn + kUnit - 1) & ~(kUnit - 1));
   };
-  // Rows of the group in block kb of the reduction (weight mode); under kBK the rest is zeroed.
-  auto rows_in = [&](const Tile& c, int kb) { return c.rows.y - c.rows.x - kb * kBK; };
+  // Rows of the group in block kb of the reduction (weight mode). Of a last
+  // block the MMAs take them in steps of 16; the rest of such a step is zeroed.
+  auto rows_in = [&](const Tile& c, int kb) { return min(c.rows.y - c.rows.x - kb * kBK, kBK); };
   const int b_cols = kPair ? a.bn / 2 : a.bn;  // columns of B in this CTA's ring
   const int b_boxes = (b_cols + 63) / 64;       // of a B that lies across
 
@@ -398,37 +418,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, tail_next = 0;
     bool stop = false;
     const uint32_t full_leader = kPair ? mapa_shared(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
-    for (long long t = first_tile; t < total && !stop; t += step) {
+    for (uint32_t t = first_tile; t < total && !stop; t += step) {
       const Tile c = tile_at(t);
       const int n0 = c.n * a.bn + (kPair ? static_cast<int>(rank) * (width_of(c) / 2) : 0);
       const int m0 = c.m * kTileM + (kPair ? static_cast<int>(rank) * kBM : 0);
-      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+      for (int kb = c.kb0; kb < c.kb1; kb += kPerStage) {
         if (!mbar_wait(&empty[s], phase ^ 1, abort_flag)) {
           raise_abort();
           stop = true;
           break;
         }
-        const bool tail = kPair && S::kWeight && rows_in(c, kb) < kBK;
+        const int blocks = min(kPerStage, c.kb1 - kb);
+        const bool tail = kPair && S::kWeight && rows_in(c, kb + blocks - 1) % 16 != 0;
         const bool own_tail = tail && !leader;
         if (elect_one()) {
-          uint8_t* da = smem + s * a.stage_bytes;
-          uint8_t* db = da + kABytes;
           const uint32_t bar = own_tail ? smem_addr(&tails[s]) : full_leader + s * 8;
           if (own_tail)
-            mbar_expect_tx(&tails[s], a.stage_bytes);
+            mbar_expect_tx(&tails[s], blocks * a.block_bytes);
           else if (leader || !kPair)
-            mbar_expect_tx(&full[s], kPair && !tail ? 2 * a.stage_bytes : a.stage_bytes);
-          if constexpr (S::kWeight) {
-            const int r = c.rows.x + kb * kBK;
+            mbar_expect_tx(&full[s], (kPair && !tail ? 2 : 1) * blocks * a.block_bytes);
+          for (int i = 0; i < blocks; ++i) {
+            uint8_t* da = smem + (s * kPerStage + i) * a.block_bytes;
+            uint8_t* db = da + kABytes;
+            const int k = kb + i;
+            if constexpr (S::kWeight) {
+              const int r = c.rows.x + k * kBK;
 #pragma unroll
-            for (int i = 0; i < kBM / 64; ++i) load_2d<kPair>(da + i * kBoxBytes, &tm_a, bar, m0 + i * 64, r);
-            for (int i = 0; i < b_boxes; ++i) load_2d<kPair>(db + i * kBoxBytes, &tm_b, bar, n0 + i * 64, r);
-          } else {
-            load_2d<kPair>(da, &tm_a, bar, kb * kBK, c.rows.x + m0);
-            if constexpr (S::kAcrossB) {
-              for (int i = 0; i < b_boxes; ++i) load_3d<kPair>(db + i * kBoxBytes, &tm_b, bar, n0 + i * 64, kb * kBK, c.e);
+              for (int j = 0; j < kBM / 64; ++j) load_2d<kPair>(da + j * kBoxBytes, &tm_a, bar, m0 + j * 64, r);
+              for (int j = 0; j < b_boxes; ++j) load_2d<kPair>(db + j * kBoxBytes, &tm_b, bar, n0 + j * 64, r);
             } else {
-              load_3d<kPair>(db, &tm_b, bar, kb * kBK, n0, c.e);
+              load_2d<kPair>(da, &tm_a, bar, k * kBK, c.rows.x + m0);
+              if constexpr (S::kAcrossB) {
+                for (int j = 0; j < b_boxes; ++j) load_3d<kPair>(db + j * kBoxBytes, &tm_b, bar, n0 + j * 64, k * kBK, c.e);
+              } else {
+                load_3d<kPair>(db, &tm_b, bar, k * kBK, n0, c.e);
+              }
             }
           }
         }
@@ -455,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = false;
     const uint64_t ring_a = operand_desc<S::kAcrossA>(smem_addr(smem));
     const uint64_t ring_b = operand_desc<S::kAcrossB>(smem_addr(smem) + kABytes);
-    auto zero_rows = [&](int have) {
-      const int chunks = (kBK - have) * 8;  // 16-byte chunks of one box
-      uint8_t* base = smem + s * a.stage_bytes + have * 128;
+    auto zero_rows = [&](int block, int have) {
+      const int chunks = (16 - have % 16) * 8;  // 16-byte chunks of one box
+      uint8_t* base = smem + (s * kPerStage + block) * a.block_bytes + have * 128;
 #pragma unroll 1
       for (int box = 0; box < kBM / 64 + b_boxes; ++box)
         for (int i = lane; i < chunks; i += 32)
@@ -465,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_shared();
       __syncwarp();
     };
-    for (long long t = first_tile; t < total && !stop; t += step) {
+    for (uint32_t t = first_tile; t < total && !stop; t += step) {
       const Tile c = tile_at(t);
       const uint32_t idesc =
           idesc_bf16_f32(kTileM, width_of(c)) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
@@ -480,22 +504,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t d_tmem = tmem + acc * kBN;
         const int k1 = S::kWeight ? min(k0 + kChainBlocks, c.kb1) : c.kb1;
-        for (int kb = k0; kb < k1; ++kb) {
-          const int have = S::kWeight ? rows_in(c, kb) : kBK;
+        for (int kb = k0; kb < k1; kb += kPerStage) {
+          const int blocks = min(kPerStage, k1 - kb);
+          const int have = S::kWeight ? rows_in(c, kb + blocks - 1) : kBK;  // of the stage's last block
           bool ok = true;
           if (kPair && !leader) {
-            if (have < kBK) {
+            if (have % 16 != 0) {
               ok = mbar_wait(&tails[s], (tail_next >> s) & 1, abort_flag);
               if (ok) {
-                zero_rows(have);
+                zero_rows(blocks - 1, have);
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&zeroed[s]), 0));
               }
               tail_next ^= 1u << s;
             }
           } else {
             ok = mbar_wait(&full[s], phase, abort_flag);
-            if (ok && have < kBK) {
-              zero_rows(have);
+            if (ok && have % 16 != 0) {
+              zero_rows(blocks - 1, have);
               if constexpr (kPair) {
                 ok = mbar_wait(&zeroed[s], (tail_next >> s) & 1, abort_flag);
                 fence_acq_rel_cluster();
@@ -504,16 +529,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (ok && elect_one()) {
               // descriptors hold addresses in 16-byte units, and no sum of them leaves its field
-              const uint32_t at = s * (a.stage_bytes >> 4);
+              uint32_t at = s * kPerStage * (a.block_bytes >> 4);
+              for (int i = 0; i < blocks; ++i, at += a.block_bytes >> 4) {
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk) {
-                const uint64_t da = ring_a + (at + kk * (S::kAcrossA ? 2048 >> 4 : 32 >> 4));
-                const uint64_t db = ring_b + (at + kk * (S::kAcrossB ? 2048 >> 4 : 32 >> 4));
-                const uint32_t add = (kb != k0) || (kk != 0);
-                if constexpr (kPair)
-                  umma_bf16_pair(d_tmem, da, db, idesc, add);
-                else
-                  umma_bf16(d_tmem, da, db, idesc, add);
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                  if (S::kWeight && i == blocks - 1 && kk * 16 >= have) break;
+                  const uint64_t da = ring_a + (at + kk * (S::kAcrossA ? 2048 >> 4 : 32 >> 4));
+                  const uint64_t db = ring_b + (at + kk * (S::kAcrossB ? 2048 >> 4 : 32 >> 4));
+                  const uint32_t add = (kb != k0) || (i != 0) || (kk != 0);
+                  if constexpr (kPair)
+                    umma_bf16_pair(d_tmem, da, db, idesc, add);
+                  else
+                    umma_bf16(d_tmem, da, db, idesc, add);
+                }
               }
               if constexpr (kPair)
                 umma_commit_pair_all(&empty[s], 0x3);
@@ -561,7 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blocks = a.bn / 32, half = (warp - 2) >> 2;
     const int b_first = half * ((blocks + 1) / 2), b_end = half ? blocks : (blocks + 1) / 2;
     uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
-    float* my_bias = s_bias + (warp - 2) * 32;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     int filled = 0;
     auto wait_acc = [&]() {
@@ -592,12 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4)) =
             make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
     };
-    for (long long t = first_tile; t < total; t += step) {
+    for (uint32_t t = first_tile; t < total; t += step) {
       const Tile c = tile_at(t);
       const int m0 = c.m * kTileM + (kPair ? static_cast<int>(rank) * kBM : 0) + q * 32;
       const int row0 = S::kWeight ? m0 : c.rows.x + m0;
       const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;  // rows from row0 to the end
-      if constexpr (S::kWeight) {
+      const bool whole = !S::kWeight || (c.kb1 > c.kb0 && c.kb1 - c.kb0 <= kChainBlocks);  // one accumulator holds the sums
+      if (S::kWeight && !whole) {
         float f[4][32];
 #pragma unroll
         for (int b = 0; b < 4; ++b)
@@ -626,10 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kSplit) {
             keep_partial(c32, f[b]);
           } else {
-            if (n0 < p.n && left > 0) finish_block<kMode>(a, f[b], c, row0, left, n0, stg, my_bias, lane, &tm_d, &tm_p);
+            if (n0 < p.n && left > 0) finish_block<kMode>(p, f[b], Row32{}, c, row0, left, n0, stg, lane);
           }
         }
       } else {
+        constexpr bool kDgrad = kMode == MatmulMode::kDgrad, kAhead = !kSplit && !S::kWeight;
+        Row32 next{};
+        if constexpr (kAhead) next = load_ahead<kDgrad>(p, row0 + lane, c.n * a.bn + b_first * 32, lane < left);
         if (!wait_acc()) break;
         const uint32_t tbase = tmem + (filled & 1) * kBN + lanes;
 #pragma unroll 1
@@ -639,13 +670,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           float f[32];
           tmem_ld32(tbase + c32 * 32, v);
+          const Row32 ahead = next;
+          if constexpr (kAhead) next = load_ahead<kDgrad>(p, row0 + lane, n0 + 32, c32 + 1 < b_end && lane < left);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
           if constexpr (kSplit)
             keep_partial(c32, f);
           else
-            finish_block<kMode>(a, f, c, row0, left, n0, stg, my_bias, lane, &tm_d, &tm_p);
+            finish_block<kMode>(p, f, ahead, c, row0, left, n0, stg, lane);
         }
         free_acc();
       }
@@ -657,7 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 2 && first_tile < total && !*abort_flag) {
       const Tile c = tile_at(first_tile);
       uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
-      float* my_bias = s_bias + (warp - 2) * 32;
       // the tile's blocks of 32 x 32 shared out over the cluster's epilogue warps
 #pragma unroll 1
       for (int b = rank * kEpiWarps + warp - 2; b < (a.bn / 32) * 4; b += split * kEpiWarps) {
@@ -667,6 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;
         if (n0 >= p.n || left <= 0) continue;
         const uint32_t row = smem_addr(smem) + b * 4096 + lane * 128;
+        Row32 ahead{};
+        if constexpr (!S::kWeight)
+          ahead = load_ahead<kMode == MatmulMode::kDgrad>(p, row0 + lane, n0, lane < left);
         float f[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] = 0.0f;
@@ -681,12 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) f[4 * j + i] += g[i];
           }
         }
-        finish_block<kMode>(a, f, c, row0, left, n0, stg, my_bias, lane, &tm_d, &tm_p);
+        finish_block<kMode>(p, f, ahead, c, row0, left, n0, stg, lane);
       }
     }
     cluster_sync();  // nobody leaves while a peer reads its shared memory
   }
-  if (warp >= 2 && lane == 0) bulk_wait_all();  // the staged stores have completed
 
   tc_fence_before();
   __syncthreads();
@@ -713,43 +747,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A tensor map of up to three dimensions (contiguous first), strides in
-// elements. Host side; false if the driver refuses it.
-bool encode(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* base, int rank, const uint64_t* dims,
-            const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
-  cuuint64_t d[3], st[2];
-  cuuint32_t b[3], one[3] = {1, 1, 1};
-  for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
-  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i] * bytes;
-  return encode_fn()(m, type, rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
+// The tensor map of an operand: cols contiguous, rows ld apart, and with
+// groups > 0 a third axis of `stride` elements; boxes of 64 columns, 128-byte
+// swizzle. False if the driver refuses it.
+bool load_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t groups,
+              uint64_t stride, uint32_t box_rows) {
+  const cuuint64_t dims[3] = {cols, rows, groups}, strides[2] = {ld * 2, stride * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1}, one[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                     one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool load_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t groups,
-              uint64_t stride, uint32_t box_rows) {
-  const uint64_t dims[3] = {cols, rows, groups}, st[2] = {ld, stride};
-  const uint32_t box[3] = {64, box_rows, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, groups ? 3 : 2, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-}
-
-bool store_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld) {
-  const uint64_t dims[2] = {cols, rows}, st[1] = {ld};
-  const uint32_t box[2] = {32, 32};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, 2, dims, st, box, CU_TENSOR_MAP_SWIZZLE_64B,
-                CU_TENSOR_MAP_L2_PROMOTION_NONE);
-}
-
 template <MatmulMode kMode, Form kForm>
-cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const CUtensorMap& tp,
-                         const TcArgs& t, long long grid, int cluster, cudaStream_t s) {
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& t, long long grid, int cluster,
+                         cudaStream_t s) {
   using S = Shape<kMode>;
   auto* kernel = matmul_tc_kernel<kMode, kForm>;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
   return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, s, true,
-                       static_cast<unsigned>(cluster), ta, tb, td, tp, t);
+                       static_cast<unsigned>(cluster), ta, tb, t);
 }
 
 // How a product is cut up.
@@ -778,19 +797,34 @@ double expected_tiles(const Problem& q, int tile) {
 // The cut with the least estimated time on the busiest SM, in nanoseconds: a
 // block of 64 along the reduction costs what it measured on B200 with all SMs
 // busy (2048 rows, 9 column tiles, k 4096 to 8192; forward, wgrad):
-//            bn 256     192        128        64
-//   kPair    374, 384   262, 341   214, 294   203, 327
-//   kSingle  413, 441   341, 379   265, 318   221, 319
+//            bn 256     128
+//   kPair    370, 433   187, 310
+//   kSingle  422, 437   250, 328
 // (narrow tiles are bound by the issue of loads and MMAs, wide ones by the
 // tensor pipe at the clock that the power limit leaves). A tile costs about
-// 500 more, a pair's start 2000, a split's exchange 1500 a CTA (clusters of 8
-// measured 25 us slower than their share: few fit beside one another).
+// 500 more, in weight mode no less than its fp32 stores (13 bn), with pairs
+// and ragged groups 1700 for the zeroed rows' handshake (2051 tokens in 128
+// groups: 256-wide single tiles 170 us, pairs 240); a pair's start 2000, a
+// split's exchange 1500 a CTA (clusters of 8 measured 25 us slower than their
+// share: few fit beside one another).
+//
+// Many ragged groups in rows mode take the widest tiles, in pairs from 1024 rows
+// a group on: their sizes are not known here, so neither is how the tiles
+// fill the last wave (skewed layer, 64 groups of 0 to 1920 rows out of 98304:
+// 256-wide pairs and single tiles 187 and 183 us, 192-wide pairs 217; 8 groups
+// of about 1000 rows 52, 57 and 61).
 Choice choose_tiles(const Problem& q, int sms) {
   Choice best{Form::kSingle, kBN, 1};
+  if (!q.weight && q.groups > 1 && q.n > kBN / 2 && expected_tiles(q, 256) * ((q.n + kBN - 1) / kBN) > sms) {
+    if (q.rows >= 1024LL * q.groups) best.form = Form::kPair;
+    return best;
+  }
   double least = 1e300;
   auto consider = [&](Form form, int bn, int split, double tiles, int units, double block, double once) {
     const double waves = std::ceil(tiles / units - 1e-9);
-    const double time = waves * ((q.blocks + split - 1) / split * block + 500) + once;
+    double tile = (q.blocks + split - 1) / split * block + 500;
+    if (q.weight) tile = std::max(tile, 13.0 * bn) + (form == Form::kPair && q.groups > 1 ? 1700 : 0);
+    const double time = waves * tile + once;
     if (time < least) {
       least = time;
       best = {form, bn, split};
@@ -799,8 +833,8 @@ Choice choose_tiles(const Problem& q, int sms) {
   for (int bn = kBN; bn >= 64; bn -= 32) {
     if (bn - 32 >= q.n && bn > 64) continue;  // wider than the matrix
     const double n_tiles = (q.n + bn - 1) / bn;
-    const double pair = q.weight ? 210 + 0.7 * bn : std::max(1.42 * bn, 160 + 0.45 * bn);
-    const double single = (q.weight ? 210 : 165) + 0.9 * bn;
+    const double pair = q.weight ? 190 + 0.95 * bn : std::max(1.44 * bn, 130 + 0.45 * bn);
+    const double single = q.weight ? 217 + 0.86 * bn : std::max(77 + 1.35 * bn, 150 + 0.78 * bn);
     consider(Form::kPair, bn, 1, expected_tiles(q, 256) * n_tiles, sms / 2, pair, 2000);
     consider(Form::kSingle, bn, 1, expected_tiles(q, 128) * n_tiles, sms, single, 0);
     for (int split = 2; split <= 4; split *= 2)
@@ -820,26 +854,18 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   const Choice choice = choose_tiles(q, sms);
   const bool pair = choice.form == Form::kPair;
   const int tile_m = pair ? 256 : 128, b_cols = pair ? choice.bn / 2 : choice.bn;
-  CUtensorMap ta, tb, td{}, tp{};
+  CUtensorMap ta, tb;
   TcArgs t{};
   t.p = a;
   t.bn = choice.bn;
   t.n_tiles = (a.n + t.bn - 1) / t.bn;
   t.m_tiles = S::kWeight ? (a.m + tile_m - 1) / tile_m : 0;
-  t.stage_bytes = kABytes + (S::kAcrossB ? (b_cols + 63) / 64 * kBoxBytes : b_cols * kBK * 2);
-  t.stages = std::min<int>(kMaxStages, kRingBytes / t.stage_bytes);
+  t.block_bytes = kABytes + (S::kAcrossB ? (b_cols + 63) / 64 * kBoxBytes : b_cols * kBK * 2);
+  t.stages = std::min<int>(kMaxStages, S::kRingBytes / (blocks_per_stage(choice.form) * t.block_bytes));
   bool ok;
   if constexpr (S::kWeight) {
     t.band = 16;
     ok = load_map(&ta, a.a, a.m, a.rows, a.lda, 0, 0, 64) && load_map(&tb, a.b, a.n, a.rows, a.ldb, 0, 0, 64);
-    t.tma_store = a.ldd % 4 == 0;
-    if (t.tma_store) {
-      const uint64_t dims[3] = {static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.m), static_cast<uint64_t>(a.groups)};
-      const uint64_t st[2] = {static_cast<uint64_t>(a.ldd), static_cast<uint64_t>(a.ldd) * a.m};
-      const uint32_t box[3] = {32, 32, 1};
-      ok = ok && encode(&td, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.d, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_NONE);
-    }
   } else {
     // a band of row tiles holds about 64 MB of A, so that it stays in L2 while the weights stream past it
     const long long tile_bytes = 2LL * tile_m * a.k;
@@ -847,19 +873,18 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
     while (t.band < (pair ? 16 : 32) && t.band * 2 * tile_bytes <= (64LL << 20)) t.band *= 2;
     constexpr bool fwd = kMode == MatmulMode::kForward;
     ok = load_map(&ta, a.a, a.k, a.rows, a.lda, 0, 0, kBM) &&
-         load_map(&tb, a.b, fwd ? a.k : a.n, fwd ? a.n : a.k, a.ldb, a.groups, a.b_stride, fwd ? b_cols : 64) &&
-         store_map(&td, a.d, a.n, a.rows, a.ldd) && (!a.preact || store_map(&tp, a.preact, a.n, a.rows, a.ldz));
-    t.tma_store = 1;
+         load_map(&tb, a.b, fwd ? a.k : a.n, fwd ? a.n : a.k, a.ldb, a.groups, a.b_stride, fwd ? b_cols : 64);
   }
   if (!ok) return cudaErrorInvalidValue;
   const long long tiles = most_tiles(q, tile_m) * t.n_tiles;
+  if (tiles >= 1LL << 31) return cudaErrorInvalidValue;
   switch (choice.form) {
     case Form::kPair:
-      return launch_tiles<kMode, Form::kPair>(ta, tb, td, tp, t, 2 * std::min<long long>(tiles, sms / 2), 2, s);
+      return launch_tiles<kMode, Form::kPair>(ta, tb, t, 2 * std::min<long long>(tiles, sms / 2), 2, s);
     case Form::kSplit:
-      return launch_tiles<kMode, Form::kSplit>(ta, tb, td, tp, t, tiles * choice.split, choice.split, s);
+      return launch_tiles<kMode, Form::kSplit>(ta, tb, t, tiles * choice.split, choice.split, s);
     default:
-      return launch_tiles<kMode, Form::kSingle>(ta, tb, td, tp, t, std::min<long long>(tiles, sms), 1, s);
+      return launch_tiles<kMode, Form::kSingle>(ta, tb, t, std::min<long long>(tiles, sms), 1, s);
   }
 }
 

@@ -163,13 +163,6 @@ MOE_DEV void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y)
                : "memory");
 }
 
-MOE_DEV void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
 // Untiled bulk copies (TMA engine, no tensor map). Addresses 16-byte aligned,
 // sizes multiples of 16 bytes.
 MOE_DEV void bulk_load(void* smem_dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {

@@ -192,7 +192,7 @@ struct MatmulArgs {
   void* d;
   int act;
   int32_t* status;
-  int vec_a, vec_b;        // strides allow four-element loads (fp32 path)
+  int vec;                 // fp32 path: widths and strides are multiples of four
 };
 // matmul_simt.cu
 cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
