@@ -67,7 +67,9 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
 }
 
 cudaError_t launch_product(int dtype, MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_F32) return launch_matmul_f32(mode, a, s);
+  if (dtype == MOE_DTYPE_F32)
+    return mode == MatmulMode::kForward && matmul_few_rows_f32(a) ? launch_matmul_rows_f32(a, s)
+                                                                  : launch_matmul_f32(mode, a, s);
   if (mode == MatmulMode::kForward && matmul_few_rows(a)) return launch_matmul_rows(a, s);
   return launch_matmul_tc(mode, a, s);
 }

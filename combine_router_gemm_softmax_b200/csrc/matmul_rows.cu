@@ -127,6 +127,82 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) matmul_rows_kernel(c
   }
 }
 
+// The same in fp32 on the CUDA cores: a warp takes a part of the reduction of
+// four features and kTokens of the group's rows (more take further blocks).
+constexpr int kF32Features = 4, kF32Warps = 8;
+
+template <int kTokens, bool kVec>
+__global__ void __launch_bounds__(32 * kF32Warps) matmul_rows_f32_kernel(const MatmulArgs a) {
+  constexpr int kShift = kTokens == 1 ? 0 : kTokens == 2 ? 1 : 2;
+  __shared__ int2 s_rows[kMaxE];
+  __shared__ int prefix[kMaxE + 1];
+  __shared__ float s_sum[kF32Warps][kF32Features * kTokens];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  int e = 0, r0 = blockIdx.y * kTokens, end = a.rows;
+  if (a.offsets != nullptr) {
+    if (warp == 0)
+      build_groups(a.offsets, a.groups, a.rows, kShift, s_rows, prefix, blockIdx.y == 0 ? a.status : nullptr, lane);
+    __syncthreads();
+    const int tile = blockIdx.y;
+    if (tile >= prefix[a.groups]) return;
+    e = group_of_tile(prefix, a.groups, tile);
+    r0 = s_rows[e].x + (tile - prefix[e]) * kTokens;
+    end = s_rows[e].y;
+  }
+  const int have = min(kTokens, end - r0), n0 = blockIdx.x * kF32Features;
+  const float* w = static_cast<const float*>(a.b) + e * a.b_stride + n0 * a.ldb;
+  const float* x = static_cast<const float*>(a.a) + static_cast<long long>(r0) * a.lda;
+  float acc[kF32Features][kTokens] = {};
+  constexpr int kStep = kVec ? 4 : 1;
+#pragma unroll 2
+  for (int k = (warp * 32 + lane) * kStep; k < a.k; k += 32 * kF32Warps * kStep) {
+    float fw[kF32Features][kStep], fx[kTokens][kStep];
+    auto load = [](float(&f)[kStep], const float* p, bool there) {
+      if constexpr (kVec) {
+        const float4 q = there ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+        f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+      } else {
+        f[0] = there ? *p : 0.0f;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kF32Features; ++i) load(fw[i], w + i * a.ldb + k, n0 + i < a.n);
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) load(fx[j], x + j * a.lda + k, j < have);
+#pragma unroll
+    for (int i = 0; i < kF32Features; ++i)
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j)
+#pragma unroll
+        for (int v = 0; v < kStep; ++v) acc[i][j] = fmaf(fw[i][v], fx[j][v], acc[i][j]);
+  }
+#pragma unroll
+  for (int i = 0; i < kF32Features; ++i)
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      float v = acc[i][j];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) s_sum[warp][j * kF32Features + i] = v;
+    }
+  __syncthreads();
+  const int token = threadIdx.x / kF32Features, n = n0 + static_cast<int>(threadIdx.x) % kF32Features;
+  if (token >= have || n >= a.n) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kF32Warps; ++q) v += s_sum[q][threadIdx.x];
+  finish_element<false>(a, v, e, static_cast<long long>(r0) + token, n);
+}
+
+template <int kTokens>
+cudaError_t launch_f32(const MatmulArgs& a, cudaStream_t s) {
+  const long long blocks = (a.rows + kTokens - 1LL) / kTokens + std::min(a.groups, a.rows) - 1;
+  return launch_kernel(a.vec ? matmul_rows_f32_kernel<kTokens, true> : matmul_rows_f32_kernel<kTokens, false>,
+                       dim3((a.n + kF32Features - 1) / kF32Features, static_cast<unsigned>(blocks)),
+                       dim3(32 * kF32Warps), 0, s, true, 1, a);
+}
+
 template <int kTiles, int kWarps>
 cudaError_t launch_features(const MatmulArgs& a, long long blocks, cudaStream_t s) {
   return launch_kernel(matmul_rows_kernel<kTiles, kWarps>,
@@ -158,6 +234,13 @@ cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s) {
   if ((a.n + 15) / 16 * blocks * 8 <= fit) return launch_features<1, 8>(a, blocks, s);
   if ((a.n + 31) / 32 * blocks * 8 <= fit) return launch_features<2, 8>(a, blocks, s);
   return launch_features<2, 4>(a, blocks, s);
+}
+
+bool matmul_few_rows_f32(const MatmulArgs& a) { return a.rows <= 8 || 2LL * a.rows <= a.groups; }
+
+cudaError_t launch_matmul_rows_f32(const MatmulArgs& a, cudaStream_t s) {
+  const int each = (a.rows + a.groups - 1) / a.groups;
+  return each == 1 ? launch_f32<1>(a, s) : each == 2 ? launch_f32<2>(a, s) : launch_f32<4>(a, s);
 }
 
 }  // namespace moe

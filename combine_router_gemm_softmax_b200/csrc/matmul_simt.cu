@@ -5,8 +5,10 @@
 // A CTA of 256 threads owns a tile of BT x BT outputs (BT 128 or 64), each
 // thread (BT/16)^2 of them in registers as pairs along n, so that one packed
 // fma.rn.f32x2 does two multiply-adds. Slices of 16 along the reduction pass
-// through two shared-memory buffers; the next slice is in flight in registers
-// while this one is multiplied. Operands are read as they lie: along the
+// through two shared-memory buffers, one barrier a slice; the next slices are
+// under way in registers (one for 128-wide tiles, whose slice takes a
+// microsecond of arithmetic, four for 64-wide ones, whose slice takes a
+// quarter of the load latency). Operands are read as they lie: along the
 // reduction or across it, by template, so no mode needs a transposed copy.
 // Bound: the fp32 pipe (128 multiply-adds a cycle and SM).
 //
@@ -115,7 +117,7 @@ MOE_DEV int at(int t, int i) {
 }
 
 template <MatmulMode kMode, bool kVec, int BT>
-__global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs a) {
+__global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 3) matmul_simt_kernel(const MatmulArgs a) {
   constexpr int kPer = BT / 16;  // outputs of a thread along each axis
   constexpr bool kWeight = kMode == MatmulMode::kWgrad;
   __shared__ __align__(16) float sA[2][kBK][BT + 4];
@@ -171,46 +173,47 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
 #pragma unroll
       for (int j = 0; j < kPer / 2; ++j) acc[i][j] = 0;
 
-    Slice<!kWeight, kVec, BT> qa;
-    Slice<kMode == MatmulMode::kForward, kVec, BT> qb;
-    if (k_first < depth) {
-      qa.load(pa, a.lda, m_valid, k_first, depth);
-      qb.load(pb, a.ldb, n_valid, k_first, depth);
-      qa.store(sA[0]);
-      qb.store(sB[0]);
+    constexpr int kAhead = BT == 128 ? 1 : 4;  // slices in registers
+    Slice<!kWeight, kVec, BT> qa[kAhead];
+    Slice<kMode == MatmulMode::kForward, kVec, BT> qb[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      qa[i].load(pa, a.lda, m_valid, k_first + i * kBK, depth);
+      qb[i].load(pb, a.ldb, n_valid, k_first + i * kBK, depth);
     }
-    __syncthreads();
     int buf = 0;
-    for (int k0 = k_first; k0 < depth; k0 += kBK, buf ^= 1) {
-      const bool more = k0 + kBK < depth;
-      if (more) {
-        qa.load(pa, a.lda, m_valid, k0 + kBK, depth);
-        qb.load(pb, a.ldb, n_valid, k0 + kBK, depth);
-      }
+    for (int k1 = k_first; k1 < depth; k1 += kAhead * kBK) {
 #pragma unroll
-      for (int k = 0; k < kBK; ++k) {
-        float ra[kPer];
-        uint64_t rb[kPer / 2];
+      for (int s = 0; s < kAhead; ++s) {
+        const int k0 = k1 + s * kBK;
+        if (k0 >= depth) break;
+        qa[s].store(sA[buf]);
+        qb[s].store(sB[buf]);
+        __syncthreads();  // also: everyone is done with the other buffer
+        qa[s].load(pa, a.lda, m_valid, k0 + kAhead * kBK, depth);
+        qb[s].load(pb, a.ldb, n_valid, k0 + kAhead * kBK, depth);
 #pragma unroll
-        for (int g = 0; g < kPer / 4; ++g) {
-          const float4 f = *reinterpret_cast<const float4*>(&sA[buf][k][at<BT>(ty, g * 4)]);
-          ra[4 * g] = f.x, ra[4 * g + 1] = f.y, ra[4 * g + 2] = f.z, ra[4 * g + 3] = f.w;
-          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sB[buf][k][at<BT>(tx, g * 4)]);
-          rb[2 * g] = u.x, rb[2 * g + 1] = u.y;
+        for (int k = 0; k < kBK; ++k) {
+          float ra[kPer];
+          uint64_t rb[kPer / 2];
+#pragma unroll
+          for (int g = 0; g < kPer / 4; ++g) {
+            const float4 f = *reinterpret_cast<const float4*>(&sA[buf][k][at<BT>(ty, g * 4)]);
+            ra[4 * g] = f.x, ra[4 * g + 1] = f.y, ra[4 * g + 2] = f.z, ra[4 * g + 3] = f.w;
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sB[buf][k][at<BT>(tx, g * 4)]);
+            rb[2 * g] = u.x, rb[2 * g + 1] = u.y;
+          }
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const uint64_t d = pack2(ra[i], ra[i]);
+#pragma unroll
+            for (int j = 0; j < kPer / 2; ++j) fma2(acc[i][j], d, rb[j]);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const uint64_t d = pack2(ra[i], ra[i]);
-#pragma unroll
-          for (int j = 0; j < kPer / 2; ++j) fma2(acc[i][j], d, rb[j]);
-        }
+        buf ^= 1;
       }
-      if (more) {
-        qa.store(sA[buf ^ 1]);
-        qb.store(sB[buf ^ 1]);
-      }
-      __syncthreads();
     }
+    __syncthreads();  // before the next tile's slices overwrite a buffer
 
     auto finish = [&](int i, int j, float v) {
       if (i >= m_valid || j >= n_valid) return;
@@ -266,13 +269,13 @@ cudaError_t launch_tiles(const MatmulArgs& a, cudaStream_t s) {
     return tm * tn;
   };
   if (tiles(128) >= sms)
-    return launch_kernel(matmul_simt_kernel<kMode, kVec, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), sms))),
+    return launch_kernel(matmul_simt_kernel<kMode, kVec, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), 2 * sms))),
                          dim3(kThreads), 0, s, true, 1, a);
   const long long t = tiles(64);
   const int depth = kMode == MatmulMode::kWgrad ? a.rows : a.k;
   int split = 1;
-  while (split < 8 && t * split * 2 <= 2 * sms && depth / (split * 2) >= 64) split *= 2;
-  const long long grid = std::min<long long>(t, 4 * sms) * split;
+  while (split < 8 && t * split * 2 <= 3 * sms && depth / (split * 2) >= 64) split *= 2;
+  const long long grid = std::min<long long>(t, 3 * sms) * split;
   return launch_kernel(matmul_simt_kernel<kMode, kVec, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, true,
                        static_cast<unsigned>(split), a);
 }

@@ -199,6 +199,9 @@ cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t
 // matmul_rows.cu: the forward for few rows a group, and whether a call is that (same demands as matmul_tc.cu)
 bool matmul_few_rows(const MatmulArgs& a);
 cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s);
+// the same in fp32 (any alignment)
+bool matmul_few_rows_f32(const MatmulArgs& a);
+cudaError_t launch_matmul_rows_f32(const MatmulArgs& a, cudaStream_t s);
 // matmul_tc.cu (strides and addresses on 16 bytes)
 cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
 // matmul_simt.cu
