@@ -16,7 +16,7 @@
 // offsets. Warp 0 loads a ring of up to 8 stages (192 KB) by TMA, one thread
 // of warp 1 issues tcgen05.mma into one of two TMEM accumulators, warps 2..9
 // drain the other: bias, activation, slope and residual in fp32, one rounding,
-// and 32 x 32 blocks through shared memory to coalesced stores. Three forms:
+// a row a thread straight to global memory. Three forms:
 //
 //   kPair    256 x bn tiles on a cluster of two CTAs (cta_group::2): each loads
 //            128 rows of A and half of B, 32 KB a stage at bn = 256, so that
@@ -77,6 +77,7 @@ struct TcArgs {
   uint32_t block_bytes;  // of one block in one CTA's ring
   int n_tiles, m_tiles;  // column tiles; weight mode: row tiles of one group
   int band;              // row tiles per band of the tile walk
+  int align_d, align_p;  // bytes that rows of D and preact start on: 32, 16, or less
 };
 
 // full, empty, tails and zeroed per stage, two accumulators' full and empty, the drain; even
@@ -87,8 +88,8 @@ struct Shape {
   static constexpr bool kWeight = kMode == MatmulMode::kWgrad;
   static constexpr bool kAcrossA = kWeight;                       // A lies across the reduction
   static constexpr bool kAcrossB = kMode != MatmulMode::kForward;  // B does
-  static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 32 * 64;  // a 32 x 32 block of the output, a warp's
   static constexpr uint32_t kRingBytes = 192 * 1024;
+  static constexpr uint32_t kStgBytes = kWeight ? 32 * 128 : 0;  // a warp's store staging
   static constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStgBytes + kBarriers * 8 + 16 +
                                   (kWeight ? 0 : (kMaxE + 1) * 4);
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -170,48 +171,64 @@ MOE_DEV float2 pair_of(const Row32& r, int i) {  // elements 2 i and 2 i + 1
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 
-// A warp's 32 x 32 block of the output, a row a lane in v, to global memory:
-// through shared memory (16-byte chunk j of row r at j ^ (r & 7), or with
-// 64-byte rows at j ^ (r / 2 & 3)), so that a store instruction writes whole
-// rows of the block (4 of 128 bytes, 8 of 64). rows, cols: what of the block
-// exists. TMA stores from the same buffers cost a proxy fence a block, on which
-// the epilogue warps of a short reduction spent most of their time.
-template <typename T>
-MOE_DEV void store_block(uint8_t* stg, const uint4 (&v)[sizeof(T) * 2], T* out, long long ld, int rows, int cols,
-                         bool vec, int lane) {
-  constexpr int kChunks = sizeof(T) * 2, kPer = 16 / sizeof(T);  // chunks of a row, elements of a chunk
-  auto place = [](int r, int j) { return r * kChunks * 16 + ((j ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
-  __syncwarp();
+// Rows mode: a lane's 32 bf16 columns of the output, `have` of which exist,
+// straight from its registers: whole 32-byte sectors where rows start on them
+// (`align`), else 16 bytes, else single elements. Staged through shared
+// memory, whose bandwidth the MMA operands and the ring's loads use up, or
+// stored by TMA, a proxy fence a block, a short reduction's blocks took longer
+// (k 512, single tiles: 3.8 us a tile against 4.5).
+MOE_DEV void store_rows(const float (&f)[32], void* base, long long at, int have, int align, bool valid) {
+  if (!valid) return;
+  uint32_t w[16];
 #pragma unroll
-  for (int j = 0; j < kChunks; ++j) *reinterpret_cast<uint4*>(stg + place(lane, j)) = v[j];
-  __syncwarp();
-  const int j = lane % kChunks, have = cols - j * kPer;
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at;
+  if (have >= 32 && align >= 32) {
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int r = i * (32 / kChunks) + lane / kChunks;
-    const uint4 q = *reinterpret_cast<const uint4*>(stg + place(r, j));
-    if (r >= rows) continue;
-    T* p = out + r * ld + j * kPer;
-    if (have >= kPer && vec) {
-      *reinterpret_cast<uint4*>(p) = q;
-    } else {
-      const T* e = reinterpret_cast<const T*>(&q);
+    for (int i = 0; i < 16; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * i), "r"(w[i]), "r"(w[i + 1]),
+                   "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+  } else if (have >= 32) {  // 16 bytes: what the entry points demand
 #pragma unroll
-      for (int x = 0; x < kPer; ++x)
-        if (x < have) p[x] = e[x];
-    }
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<uint4*>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < have) p[i] = __float2bfloat16_rn(f[i]);
   }
 }
 
-// The same for sums rounded to bf16 here.
-MOE_DEV void store_rows(uint8_t* stg, const float (&f)[32], void* base, long long at, long long ld, int rows, int cols,
-                        int lane) {
-  uint4 v[4];
+// Weight mode: a warp's 32 x 32 block of fp32, a row a lane, through shared
+// memory (16-byte chunk j of row r at j ^ (r & 7)), so that a store instruction
+// writes 4 whole rows of 128 bytes. With many short groups the stores are what
+// bounds the kernel, and 32-byte pieces of 32 rows an instruction cost 17%
+// there (2051 tokens in 128 groups: 322 us against 275, both gradients).
+MOE_DEV void store_block(uint8_t* stg, const float (&f)[32], float* out, long long ld, int rows, int cols, bool vec,
+                         int lane) {
+  auto place = [](int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); };
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                      pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
-  store_block(stg, v, static_cast<__nv_bfloat16*>(base) + at, ld, rows, cols, true, lane);
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4*>(stg + place(lane, j)) = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+  __syncwarp();
+  const int j = lane & 7, have = cols - j * 4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    const float4 q = *reinterpret_cast<const float4*>(stg + place(r, j));
+    if (r >= rows) continue;
+    float* p = out + r * ld + j * 4;
+    if (have >= 4 && vec) {
+      *reinterpret_cast<float4*>(p) = q;
+    } else {
+      if (have > 0) p[0] = q.x;
+      if (have > 1) p[1] = q.y;
+      if (have > 2) p[2] = q.z;
+      if (have > 3) p[3] = q.w;
+    }
+  }
 }
 
 // What the epilogue of a rows-mode block reads besides the sums, loaded ahead
@@ -226,8 +243,11 @@ MOE_DEV Row32 load_ahead(const MatmulArgs& p, long long r, int n0, bool valid) {
 // The epilogue of one 32 x 32 block of rows mode: rows row0 .. of which the
 // group has `left`, this lane's the lane-th; columns n0 ..; sums in f.
 template <bool kDgrad>
-MOE_DEV void finish_rows(const MatmulArgs& p, float (&f)[32], const Row32& ahead, int e, long long row0, int left, int n0,
-                         uint8_t* stg, int lane) {
+MOE_DEV void finish_rows(const TcArgs& a, float (&f)[32], const Row32& ahead, int e, long long row0, int left, int n0,
+                         int lane) {
+  const MatmulArgs& p = a.p;
+  const long long r = row0 + lane;
+  const bool valid = lane < left;
   if constexpr (kDgrad) {
     if (p.z != nullptr) {
       with_act(p.act, [&](auto k) {
@@ -245,7 +265,7 @@ MOE_DEV void finish_rows(const MatmulArgs& p, float (&f)[32], const Row32& ahead
 #pragma unroll
       for (int i = 0; i < 32; ++i) f[i] += __shfl_sync(0xffffffffu, b, i);
     }
-    if (p.preact != nullptr) store_rows(stg, f, p.preact, row0 * p.ldz + n0, p.ldz, left, p.n - n0, lane);
+    if (p.preact != nullptr) store_rows(f, p.preact, r * p.ldz + n0, p.n - n0, a.align_p, valid);
     if (p.act != MOE_ACT_NONE)
       with_act(p.act, [&](auto k) {
 #pragma unroll
@@ -254,7 +274,7 @@ MOE_DEV void finish_rows(const MatmulArgs& p, float (&f)[32], const Row32& ahead
   }
   if (p.residual != nullptr) {
     const Row32 res = kDgrad && p.z != nullptr
-                          ? load_row(p.residual, (row0 + lane) * p.ldr + n0, n0, p.n, lane < left)
+                          ? load_row(p.residual, r * p.ldr + n0, n0, p.n, valid)
                           : ahead;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -263,23 +283,19 @@ MOE_DEV void finish_rows(const MatmulArgs& p, float (&f)[32], const Row32& ahead
       f[2 * i + 1] += t.y;
     }
   }
-  store_rows(stg, f, p.d, row0 * p.ldd + n0, p.ldd, left, p.n - n0, lane);
+  store_rows(f, p.d, r * p.ldd + n0, p.n - n0, a.align_d, valid);
 }
 
 // One 32 x 32 block to its epilogue (weight mode: fp32 rows of group e's gradient).
 template <MatmulMode kMode>
-MOE_DEV void finish_block(const MatmulArgs& p, float (&f)[32], const Row32& ahead, const Tile& c, int row0, int left,
-                          int n0, uint8_t* stg, int lane) {
+MOE_DEV void finish_block(const TcArgs& a, float (&f)[32], const Row32& ahead, const Tile& c, int row0, int left, int n0,
+                          uint8_t* stg, int lane) {
   if constexpr (Shape<kMode>::kWeight) {
-    uint4 v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
-                        __float_as_uint(f[4 * j + 3]));
-    store_block(stg, v, static_cast<float*>(p.d) + (static_cast<long long>(c.e) * p.m + row0) * p.ldd + n0, p.ldd, left,
-                p.n - n0, p.ldd % 4 == 0, lane);
+    const MatmulArgs& p = a.p;
+    store_block(stg, f, static_cast<float*>(p.d) + (static_cast<long long>(c.e) * p.m + row0) * p.ldd + n0, p.ldd, left,
+                p.n - n0, a.align_d >= 16, lane);
   } else {
-    finish_rows<kMode == MatmulMode::kDgrad>(p, f, ahead, c.e, row0, left, n0, stg, lane);
+    finish_rows<kMode == MatmulMode::kDgrad>(a, f, ahead, c.e, row0, left, n0, lane);
   }
 }
 
@@ -654,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kSplit) {
             keep_partial(c32, f[b]);
           } else {
-            if (n0 < p.n && left > 0) finish_block<kMode>(p, f[b], Row32{}, c, row0, left, n0, stg, lane);
+            if (n0 < p.n && left > 0) finish_block<kMode>(a, f[b], Row32{}, c, row0, left, n0, stg, lane);
           }
         }
       } else {
@@ -678,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kSplit)
             keep_partial(c32, f);
           else
-            finish_block<kMode>(p, f, ahead, c, row0, left, n0, stg, lane);
+            finish_block<kMode>(a, f, ahead, c, row0, left, n0, stg, lane);
         }
         free_acc();
       }
@@ -689,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();  // every partial tile is in place
     if (warp >= 2 && first_tile < total && !*abort_flag) {
       const Tile c = tile_at(first_tile);
-      uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
+        uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
       // the tile's blocks of 32 x 32 shared out over the cluster's epilogue warps
 #pragma unroll 1
       for (int b = rank * kEpiWarps + warp - 2; b < (a.bn / 32) * 4; b += split * kEpiWarps) {
@@ -716,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) f[4 * j + i] += g[i];
           }
         }
-        finish_block<kMode>(p, f, ahead, c, row0, left, n0, stg, lane);
+        finish_block<kMode>(a, f, ahead, c, row0, left, n0, stg, lane);
       }
     }
     cluster_sync();  // nobody leaves while a peer reads its shared memory
@@ -778,7 +794,7 @@ struct Choice {
 };
 
 struct Problem {
-  bool weight;
+  bool weight, across;  // weight mode; B lies across the reduction
   long long rows;  // tiled rows: of D in all groups, or of one group's D (weight mode)
   int groups, n, blocks;
 };
@@ -835,7 +851,9 @@ Choice choose_tiles(const Problem& q, int sms) {
     const double n_tiles = (q.n + bn - 1) / bn;
     const double pair = q.weight ? 190 + 0.95 * bn : std::max(1.44 * bn, 130 + 0.45 * bn);
     const double single = q.weight ? 217 + 0.86 * bn : std::max(77 + 1.35 * bn, 150 + 0.78 * bn);
-    consider(Form::kPair, bn, 1, expected_tiles(q, 256) * n_tiles, sms / 2, pair, 2000);
+    // a B that lies across is loaded in whole boxes of 64 columns
+    if (!q.across || bn % 128 == 0) consider(Form::kPair, bn, 1, expected_tiles(q, 256) * n_tiles, sms / 2, pair, 2000);
+    if (q.across && bn % 64 != 0) continue;
     consider(Form::kSingle, bn, 1, expected_tiles(q, 128) * n_tiles, sms, single, 0);
     for (int split = 2; split <= 4; split *= 2)
       if (most_tiles(q, 128) * n_tiles * split <= sms && q.blocks >= 2 * split)
@@ -850,7 +868,7 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
   const int sms = device_sm_count();
   const int depth = S::kWeight ? (a.rows + a.groups - 1) / a.groups : a.k;
-  const Problem q{S::kWeight, S::kWeight ? a.m : a.rows, a.groups, a.n, (depth + kBK - 1) / kBK};
+  const Problem q{S::kWeight, S::kAcrossB, S::kWeight ? a.m : a.rows, a.groups, a.n, (depth + kBK - 1) / kBK};
   const Choice choice = choose_tiles(q, sms);
   const bool pair = choice.form == Form::kPair;
   const int tile_m = pair ? 256 : 128, b_cols = pair ? choice.bn / 2 : choice.bn;
@@ -862,6 +880,13 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   t.m_tiles = S::kWeight ? (a.m + tile_m - 1) / tile_m : 0;
   t.block_bytes = kABytes + (S::kAcrossB ? (b_cols + 63) / 64 * kBoxBytes : b_cols * kBK * 2);
   t.stages = std::min<int>(kMaxStages, S::kRingBytes / (blocks_per_stage(choice.form) * t.block_bytes));
+  const int bytes = S::kWeight ? 4 : 2;
+  auto align_of = [&](const void* p, long long ld) {
+    const uint64_t u = reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * bytes;
+    return u % 32 == 0 ? 32 : u % 16 == 0 ? 16 : bytes;
+  };
+  t.align_d = align_of(a.d, a.ldd);
+  t.align_p = align_of(a.preact, a.ldz);
   bool ok;
   if constexpr (S::kWeight) {
     t.band = 16;
