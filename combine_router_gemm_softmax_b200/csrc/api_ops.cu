@@ -42,6 +42,9 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   if (c.act < MOE_ACT_NONE || c.act > MOE_ACT_SILU) return p;
   if (dense && c.groups != 1) return p;
   p.rc = MOE_ERR_UNSUPPORTED;
+  // row and column indices stay below 2^31, a tile past the last one included
+  constexpr int32_t kMost = INT32_MAX - 1024;
+  if (c.rows > kMost || c.n > kMost || c.k > kMost) return p;
   if (c.groups > MOE_MAX_E || static_cast<int64_t>(c.groups) * c.n >= (1LL << 31)) return p;
   if (c.ldx == 0) c.ldx = c.k;
   if (c.ldw == 0) c.ldw = c.k;
@@ -82,7 +85,7 @@ int forward(const moe_gemm_config* cfg, bool dense, const void* x, const int32_t
   const moe_gemm_config& c = p.c;
   if (!w || (!dense && !offsets) || (c.rows > 0 && (!x || !y))) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(preact, 16) ||
-      !aligned(bias, 16) || !aligned(offsets, 4) || !aligned(status, 4))
+      !aligned(bias, 4) || !aligned(offsets, 4) || !aligned(status, 4))
     return MOE_ERR_UNSUPPORTED;
   if (c.rows == 0) return MOE_OK;
   MatmulArgs a{};
@@ -91,6 +94,7 @@ int forward(const moe_gemm_config* cfg, bool dense, const void* x, const int32_t
   a.bias = bias, a.preact = preact, a.residual = residual, a.ldz = c.ldz, a.ldr = c.ldr;
   a.d = y, a.act = c.act, a.status = status;
   a.vec = c.k % 4 == 0 && c.ldx % 4 == 0 && c.ldw % 4 == 0 && c.w_stride % 4 == 0;
+  a.vec_out = c.ldy % 4 == 0 && (!residual || c.ldr % 4 == 0) && (!preact || c.ldz % 4 == 0);
   return rc_of(launch_product(c.dtype, MatmulMode::kForward, a, s));
 }
 
@@ -110,6 +114,7 @@ int dgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
   a.z = z, a.residual = residual, a.ldz = c.ldz, a.ldr = c.ldr;
   a.d = dx, a.act = c.act, a.status = status;
   a.vec = c.n % 4 == 0 && c.k % 4 == 0 && c.ldy % 4 == 0 && c.ldw % 4 == 0 && c.w_stride % 4 == 0;
+  a.vec_out = c.ldx % 4 == 0 && (!residual || c.ldr % 4 == 0) && (!z || c.ldz % 4 == 0);
   return rc_of(launch_product(c.dtype, MatmulMode::kDgrad, a, s));
 }
 
@@ -119,7 +124,7 @@ int wgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
   if (p.rc != MOE_OK) return p.rc;
   const moe_gemm_config& c = p.c;
   if ((!dense && !offsets) || (c.rows > 0 && (!dy || !x))) return MOE_ERR_INVALID_ARG;
-  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(dbias, 16) || !aligned(offsets, 4) ||
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 4) || !aligned(dbias, 4) || !aligned(offsets, 4) ||
       !aligned(status, 4))
     return MOE_ERR_UNSUPPORTED;
   // no rows at all: the gradients are zero (every group is empty whatever the offsets hold)
@@ -135,6 +140,7 @@ int wgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
     a.m = c.n, a.n = c.k, a.lda = c.ldy, a.ldb = c.ldx, a.ldd = c.k;
     a.d = dw, a.status = status;
     a.vec = c.n % 4 == 0 && c.k % 4 == 0 && c.ldy % 4 == 0 && c.ldx % 4 == 0;
+    a.vec_out = c.k % 4 == 0 && aligned(dw, 16);
     const int rc = rc_of(launch_product(c.dtype, MatmulMode::kWgrad, a, s));
     if (rc != MOE_OK) return rc;
   }

@@ -1186,6 +1186,8 @@ cudaError_t launch_grouped_gemm_tc(const CUtensorMap& tm_a, const CUtensorMap& t
 
 void debug_stall_next_gemms(int n) { g_stall_gemms.store(n > 0 ? n : 0); }
 
+int take_gemm_stall() { return take_stall(); }
+
 cudaError_t launch_grouped_gemm_combine(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const int32_t* offsets, int E,
                                         int K, int d, void* y_perm, const int32_t* perm_src, const int32_t* dest_row,
                                         const float* gate, int32_t* pair_cnt, void* y, int k, int32_t* status, bool pdl,

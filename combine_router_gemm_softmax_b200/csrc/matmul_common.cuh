@@ -230,21 +230,61 @@ MOE_DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// One fp32 output element of rows mode from its sum: forward
-// act(sum + bias) + residual (the pre-activation stored first), input
-// gradient sum * act'(z) + residual.
-template <bool kDgrad>
-MOE_DEV void finish_element(const MatmulArgs& a, float sum, int e, long long r, int n) {
-  float v = sum;
-  if constexpr (kDgrad) {
-    if (a.z != nullptr) v *= act_slope<false>(static_cast<const float*>(a.z)[r * a.ldz + n], a.act);
+// Up to four neighbouring fp32 outputs of rows mode from their sums (`have`
+// exist): forward act(sum + bias) + residual (the pre-activation stored first),
+// input gradient sum * act'(z) + residual. kVec: all four exist and every
+// matrix can be read and written 16 bytes at a time.
+template <bool kVec>
+MOE_DEV void load_outputs(const float* p, int have, float (&f)[4]) {
+  if constexpr (kVec) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
   } else {
-    if (a.bias != nullptr) v += a.bias[static_cast<size_t>(e) * a.n + n];
-    if (a.preact != nullptr) static_cast<float*>(a.preact)[r * a.ldz + n] = v;
-    v = act_of<false>(v, a.act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < have ? p[i] : 0.0f;
   }
-  if (a.residual != nullptr) v += static_cast<const float*>(a.residual)[r * a.ldr + n];
-  static_cast<float*>(a.d)[r * a.ldd + n] = v;
+}
+
+template <bool kVec>
+MOE_DEV void store_outputs(float* p, int have, const float (&f)[4]) {
+  if constexpr (kVec) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < have) p[i] = f[i];
+  }
+}
+
+template <bool kDgrad, bool kVec>
+MOE_DEV void finish_outputs(const MatmulArgs& a, float (&f)[4], int e, long long r, int n, int have) {
+  float res[4], z[4], b[4];
+  if (a.residual != nullptr) load_outputs<kVec>(static_cast<const float*>(a.residual) + r * a.ldr + n, have, res);
+  if constexpr (kDgrad) {
+    if (a.z != nullptr) {
+      load_outputs<kVec>(static_cast<const float*>(a.z) + r * a.ldz + n, have, z);
+      with_act(a.act, [&](auto k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] *= slope_value<decltype(k)::value, false>(z[i]);
+      });
+    }
+  } else {
+    if (a.bias != nullptr) {
+      load_outputs<false>(a.bias + static_cast<size_t>(e) * a.n + n, have, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] += b[i];
+    }
+    if (a.preact != nullptr) store_outputs<kVec>(static_cast<float*>(a.preact) + r * a.ldz + n, have, f);
+    with_act(a.act, [&](auto k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = act_value<decltype(k)::value, false>(f[i]);
+    });
+  }
+  if (a.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] += res[i];
+  }
+  store_outputs<kVec>(static_cast<float*>(a.d) + r * a.ldd + n, have, f);
 }
 
 }  // namespace moe

@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(32 * kF32Warps) matmul_rows_f32_kernel(const M
   float v = 0.0f;
 #pragma unroll
   for (int q = 0; q < kF32Warps; ++q) v += s_sum[q][threadIdx.x];
-  finish_element<false>(a, v, e, static_cast<long long>(r0) + token, n);
+  float f[4] = {v, 0.0f, 0.0f, 0.0f};
+  finish_outputs<false, false>(a, f, e, static_cast<long long>(r0) + token, n, 1);
 }
 
 template <int kTokens>
@@ -215,14 +216,18 @@ cudaError_t launch_features(const MatmulArgs& a, long long blocks, cudaStream_t 
 // Row blocks: at most, however the rows fall to the groups.
 static long long row_blocks(const MatmulArgs& a) { return (a.rows + 7LL) / 8 + std::min(a.groups, a.rows) - 1; }
 
-// Where this kernel measured faster than the tiles (us, here / there): one
-// block a group (k 4096, n 14336, 1-8 rows 24.1 / 28.1; k 1408, n 2048 3.5 /
-// 8.5; 2 tokens of 8 experts each out of 128 13.4 / 26.1), and several blocks
-// of one group while reading its weights again from L2 stays cheap (k 1408, n
-// 2048, 64 rows: 46 MB of reads 8.0 / 8.8, 96 rows: 69 MB 14.1 / 8.9; k = n =
-// 4096, 24 rows: 100 MB 15.5 / 13.9).
+// Where this kernel measured faster than the tiles (us, here / there):
+//  - one block a group: k 4096, n 14336, 1-8 rows 24.1 / 28.1; k 1408, n 2048
+//    3.5 / 8.5; 2 tokens of 8 experts each out of 128 13.4 / 26.1;
+//  - several blocks that read a group's weights again from L2, while all of
+//    them run at once: on half of the SMs' warps k = n = 4096, 16 rows
+//    11.2 / 13.7, k 2048, n 16, 2048 rows 3.8 / 9.9 (k 128, n 640, 256 rows, more
+//    than one wave: 6.3 / 3.6); on all of them if the reads stay small: k 1408,
+//    n 2048, 64 rows, 46 MB 8.0 / 8.8 (k = n = 4096, 24 rows, 100 MB 15.5 / 13.9).
 bool matmul_few_rows(const MatmulArgs& a) {
-  return a.rows <= 8 || 2LL * a.rows <= a.groups || row_blocks(a) * a.n * static_cast<long long>(a.k) <= (24LL << 20);
+  if (a.rows <= 8 || 2LL * a.rows <= a.groups) return true;
+  const long long blocks = row_blocks(a), warps = (a.n + 31) / 32 * 4 * blocks, sms = device_sm_count();
+  return warps <= 7 * sms || (warps <= 16 * sms && blocks * a.n * a.k <= (24LL << 20));
 }
 
 cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s) {

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 3) matmul_simt_kerne
         __syncthreads();  // also: everyone is done with the other buffer
         qa[s].load(pa, a.lda, m_valid, k0 + kAhead * kBK, depth);
         qb[s].load(pb, a.ldb, n_valid, k0 + kAhead * kBK, depth);
-#pragma unroll
+#pragma unroll(BT == 128 ? 16 : 8)
         for (int k = 0; k < kBK; ++k) {
           float ra[kPer];
           uint64_t rb[kPer / 2];
@@ -215,44 +215,68 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 3) matmul_simt_kerne
     }
     __syncthreads();  // before the next tile's slices overwrite a buffer
 
-    auto finish = [&](int i, int j, float v) {
-      if (i >= m_valid || j >= n_valid) return;
-      if constexpr (kWeight)
-        static_cast<float*>(a.d)[(static_cast<long long>(e) * a.m + m0 + i) * a.ldd + n0 + j] = v;
-      else
-        finish_element<kMode == MatmulMode::kDgrad>(a, v, e, m0 + i, n0 + j);
+    // four neighbouring outputs of the tile: row i, columns j ..
+    auto finish = [&](int i, int j, float(&f)[4]) {
+      const int have = n_valid - j;
+      if (i >= m_valid || have <= 0) return;
+      if constexpr (kWeight) {
+        float* d = static_cast<float*>(a.d) + (static_cast<long long>(e) * a.m + m0 + i) * a.ldd + n0 + j;
+        if (have >= 4 && a.vec_out)
+          store_outputs<true>(d, 4, f);
+        else
+          store_outputs<false>(d, have, f);
+      } else if (have >= 4 && a.vec_out) {
+        finish_outputs<kMode == MatmulMode::kDgrad, true>(a, f, e, m0 + i, n0 + j, 4);
+      } else {
+        finish_outputs<kMode == MatmulMode::kDgrad, false>(a, f, e, m0 + i, n0 + j, have);
+      }
     };
-    if (BT == 64 && split > 1) {
-      // partial tiles side by side in the cluster's shared memory, each CTA
-      // adding and finishing its share of the rows
+    if constexpr (BT == 64) {
+      // Through shared memory: the tile's rows are finished whole by neighbouring
+      // threads in a short loop (unrolled over a thread's own outputs, the
+      // activations' code outlasted a small product). With a split, the partial
+      // tiles lie side by side in the cluster's shared memory, and each CTA adds
+      // and finishes its share of the rows.
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
 #pragma unroll
         for (int j = 0; j < kPer / 2; ++j)
           *reinterpret_cast<float2*>(&s_part[at<BT>(ty, i) * 64 + at<BT>(tx, 2 * j)]) = unpack2(acc[i][j]);
-      cluster_sync();
+      if (split > 1)
+        cluster_sync();
+      else
+        __syncthreads();
       const uint32_t mine = smem_addr(s_part);
       const int first = 64 * 64 / 4 * part / split, last = 64 * 64 / 4 * (part + 1) / split;
+#pragma unroll 1
       for (int q = first + threadIdx.x; q < last; q += kThreads) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        for (uint32_t c = 0; c < split; ++c) {
-          float f[4];
-          ld_shared_cluster_v4(mapa_shared(mine + q * 16, c), f);
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (split > 1) {
+          for (uint32_t c = 0; c < split; ++c) {
+            float g[4];
+            ld_shared_cluster_v4(mapa_shared(mine + q * 16, c), g);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[x] += f[x];
+            for (int x = 0; x < 4; ++x) f[x] += g[x];
+          }
+        } else {
+          const float4 g = *reinterpret_cast<const float4*>(&s_part[q * 4]);
+          f[0] = g.x, f[1] = g.y, f[2] = g.z, f[3] = g.w;
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) finish(q >> 4, (q & 15) * 4 + x, s[x]);
+        finish(q >> 4, (q & 15) * 4, f);
       }
-      cluster_sync();  // nobody overwrites or leaves while a peer still reads
+      // nobody overwrites or leaves while somebody still reads
+      if (split > 1)
+        cluster_sync();
+      else
+        __syncthreads();
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
 #pragma unroll
-        for (int j = 0; j < kPer / 2; ++j) {
-          const float2 f = unpack2(acc[i][j]);
-          finish(at<BT>(ty, i), at<BT>(tx, 2 * j), f.x);
-          finish(at<BT>(ty, i), at<BT>(tx, 2 * j + 1), f.y);
+        for (int g = 0; g < kPer / 4; ++g) {
+          const float2 lo = unpack2(acc[i][2 * g]), hi = unpack2(acc[i][2 * g + 1]);
+          float f[4] = {lo.x, lo.y, hi.x, hi.y};
+          finish(at<BT>(ty, i), at<BT>(tx, 4 * g), f);
         }
     }
   }

@@ -77,6 +77,7 @@ struct TcArgs {
   uint32_t block_bytes;  // of one block in one CTA's ring
   int n_tiles, m_tiles;  // column tiles; weight mode: row tiles of one group
   int band;              // row tiles per band of the tile walk
+  int stall;             // testing hook: the MMA warp first waits on a barrier that nothing signals
   int align_d, align_p;  // bytes that rows of D and preact start on: 32, 16, or less
 };
 
@@ -495,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = false;
     const uint64_t ring_a = operand_desc<S::kAcrossA>(smem_addr(smem));
     const uint64_t ring_b = operand_desc<S::kAcrossB>(smem_addr(smem) + kABytes);
+    if (a.stall && !mbar_wait(drain, 0, abort_flag)) stop = true;  // nothing arrives on `drain` before the end
     auto zero_rows = [&](int block, int have) {
       const int chunks = (16 - have % 16) * 8;  // 16-byte chunks of one box
       uint8_t* base = smem + (s * kPerStage + block) * a.block_bytes + have * 128;
@@ -877,6 +879,7 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   t.p = a;
   t.bn = choice.bn;
   t.n_tiles = (a.n + t.bn - 1) / t.bn;
+  t.stall = take_gemm_stall();
   t.m_tiles = S::kWeight ? (a.m + tile_m - 1) / tile_m : 0;
   t.block_bytes = kABytes + (S::kAcrossB ? (b_cols + 63) / 64 * kBoxBytes : b_cols * kBK * 2);
   t.stages = std::min<int>(kMaxStages, S::kRingBytes / (blocks_per_stage(choice.form) * t.block_bytes));

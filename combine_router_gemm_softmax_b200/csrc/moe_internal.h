@@ -93,6 +93,7 @@ cudaError_t launch_grouped_gemm_combine(const CUtensorMap& tm_a, const CUtensorM
 // Testing hook: the next n launches of the bf16 grouped GEMM kernel stall their
 // MMA issuer on a barrier nothing signals until the bounded wait gives up.
 void debug_stall_next_gemms(int n);
+int take_gemm_stall();  // 1 if the launch being prepared is one of those
 // GEMM1 recomputed with the SwiGLU backward in its epilogue: from the gate and
 // up pre-activations of each row (x_perm rows against w13) and dh_mid [rows, F]
 // it writes dgu [rows, 2F] = [dgate | dup] in w13's interleaved column order,
@@ -192,7 +193,7 @@ struct MatmulArgs {
   void* d;
   int act;
   int32_t* status;
-  int vec;                 // fp32 path: widths and strides are multiples of four
+  int vec, vec_out;        // fp32 path: operands' (outputs' and what is added to them) widths and strides are multiples of four
 };
 // matmul_simt.cu
 cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);

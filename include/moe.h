@@ -423,8 +423,8 @@ MOE_API int32_t moe_pack_weights_mxfp8(const moe_config* cfg, const void* w13_pa
 
 /* moe_debug_stall_next_gemms -- testing hook for the timeout path. The pages
  * have no counterpart. The next n launches (process-wide, any stream) of the
- * bf16 grouped GEMM kernels (single-CTA or CTA-pair tiles) make their
- * MMA-issuing thread first wait on a barrier that nothing signals. That wait gives up after the library's
+ * bf16 grouped GEMM kernels (single-CTA or CTA-pair tiles, the layer's and
+ * those of the free products that use tensor-core tiles) make their MMA-issuing thread first wait on a barrier that nothing signals. That wait gives up after the library's
  * on-chip limit (2 s), the kernel unwinds as after any timeout (no MMA was
  * issued; the operand loads already issued are waited for and TMEM is freed)
  * and MOE_STATUS_TIMEOUT is OR-ed into the status word; that call's outputs
@@ -444,10 +444,13 @@ MOE_API int32_t moe_debug_stall_next_gemms(int32_t n);
  * they were. Sums, bias, activation and residual are fp32, rounded once each
  * to y and preact. fp32 products run on the CUDA cores in IEEE fp32, bf16
  * ones on tensor cores. No workspace. Deterministic.
- * Limits: 1 <= groups <= MOE_MAX_E, n, k >= 1, n * groups < 2^31.
+ * No other operand may overlap an output.
+ * Limits: 1 <= groups <= MOE_MAX_E, n, k >= 1, n * groups < 2^31, rows, n and
+ * k at most 2^31 - 1025.
  * Errors: MOE_ERR_INVALID_ARG (NULL, negative sizes, a stride below its
  * width, unknown act or dtype), MOE_ERR_UNSUPPORTED (limits, a pointer off 16
- * bytes, a bf16 stride that is no multiple of 8). rows == 0 is MOE_OK. */
+ * bytes (bias, dw, dbias, offsets: 4), a bf16 stride that is no multiple of
+ * 8). rows == 0 is MOE_OK. */
 MOE_API int32_t moe_grouped_gemm(const moe_gemm_config* cfg, const void* x, const int32_t* offsets, const void* w,
                                  const float* bias, const void* residual, void* preact, void* y, int32_t* status_dev,
                                  moe_stream_t stream);

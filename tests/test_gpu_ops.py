@@ -323,6 +323,109 @@ def test_same_call_gives_the_same_bits_in_place_and_under_capture(dt):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_many_short_rows(dt):
+    """Far more row blocks than a grid's second axis holds, at the smallest widths."""
+    g = torch.Generator().manual_seed(15)
+    for sizes in ([700001], [300000, 0, 1, 400000]):
+        off = offsets_of(sizes)
+        o = torch.tensor(off, dtype=torch.int32, device=DEV)
+        x, w = matrix((off[-1], 8), dt, g), matrix((len(sizes), 8, 8), dt, g)
+        y = M.moe_grouped_gemm(x, o, w)
+        for e, (a, b) in R.groups(off):
+            u, s = x[a:b].double() @ w[e].double().T, x[a:b].double().abs() @ w[e].double().abs().T
+            assert bool(((y[a:b].double() - u).abs() <= rounded(sum_error(8, s), u, dt)).all())
+        dw = M.moe_grouped_gemm_wgrad(y, o, x)
+        for e, (a, b) in R.groups(off):
+            u, s = y[a:b].double().T @ x[a:b].double(), y[a:b].double().abs().T @ x[a:b].double().abs()
+            assert bool(((dw[e].double() - u).abs() <= rounded(sum_error(b - a, s), u, F32)).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_operands_apart_and_off_their_usual_alignment(dt):
+    """Groups of W further apart than their rows are, fp32 operands on 4 bytes, outputs on 16 bytes but not 32."""
+    g = torch.Generator().manual_seed(16)
+    off = offsets_of([100, 3, 180])
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    rows, k, n = off[-1], 72, 88
+    x, dy, res = matrix((rows, k), dt, g), matrix((rows, n), dt, g), matrix((rows, n), dt, g)
+    w = matrix((3, n, k), dt, g)
+    bias = torch.randn((3, n), generator=g).to(DEV)
+    ref = M.moe_grouped_gemm(x, o, w, bias=bias, act="silu", residual=res)
+    dref, wref = M.moe_grouped_gemm_dgrad(dy, o, w), M.moe_grouped_gemm_wgrad(dy, o, x)
+    space = torch.full((3 * (n * 80 + 24),), math.nan, dtype=dt, device=DEV)
+    apart = torch.as_strided(space, (3, n, k), (n * 80 + 24, 80, 1))
+    apart.copy_(w)
+    odd = torch.empty(3 * n + 1, device=DEV)[1:].view(3, n)
+    odd.copy_(bias)
+    y = torch.empty(rows * n + 8, dtype=dt, device=DEV)[16 // x.element_size():][:rows * n].view(rows, n)
+    assert y.data_ptr() % 32 == 16
+    assert torch.equal(M.moe_grouped_gemm(x, o, apart, bias=odd, act="silu", residual=res, y=y), ref)
+    assert torch.equal(M.moe_grouped_gemm_dgrad(dy, o, apart), dref)
+    dw = torch.empty(3 * n * k + 1, device=DEV)[1:].view(3, n, k)
+    db = torch.empty(3 * n + 1, device=DEV)[1:].view(3, n)
+    assert torch.equal(M.moe_grouped_gemm_wgrad(dy, o, x, dw=dw, dbias=db), wref)
+    # a residual whose rows lie apart from the output's
+    wide = torch.zeros((rows, n + 8), dtype=dt, device=DEV)[:, :n]
+    wide.copy_(res)
+    assert torch.equal(M.moe_grouped_gemm(x, o, w, bias=bias, act="silu", residual=wide), ref)
+
+
+@pytest.mark.parametrize("rows,k,n,tiles", [(200, 640, 128, False), (1100, 640, 128, False), (640, 4096, 264, True),
+                                            (4099, 1032, 1408, True)])
+def test_a_wait_that_runs_out_is_reported(rows, k, n, tiles):
+    """The tensor-core tiles' timeout path on every way a product is cut up:
+    the MMA warp waits on a barrier that nothing signals until its limit, the
+    call ends with the status bit, and the next one is right. (The forward of
+    few rows, tiles = False, has no wait that could run out.)"""
+    g = torch.Generator().manual_seed(17)
+    x, w, dy = matrix((rows, k), BF16, g), matrix((n, k), BF16, g), matrix((rows, n), BF16, g)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    calls = (lambda: M.moe_linear(x, w, status=status), lambda: M.moe_linear_dgrad(dy, w, status=status),
+             lambda: M.moe_linear_wgrad(dy, x, status=status))
+    for i, call in enumerate(calls):
+        ref = call().clone()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        assert M.lib().moe_debug_stall_next_gemms(1) == M.MOE_OK
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            M.lib().moe_debug_stall_next_gemms(0)
+        assert int(status.item()) == (M.MOE_STATUS_TIMEOUT if tiles or i > 0 else 0)
+        status.zero_()
+        assert torch.equal(call(), ref)
+        assert int(status.item()) == 0
+
+
+def test_calls_side_by_side_do_not_disturb_one_another():
+    """The same products on two streams at once, many times over, and dropout between them."""
+    g = torch.Generator().manual_seed(18)
+    off = offsets_of([70, 0, 400, 33])
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    x, w, dy = matrix((off[-1], 520), BF16, g), matrix((4, 264, 520), BF16, g), matrix((off[-1], 264), BF16, g)
+    few, rng = matrix((4, 520), BF16, g), torch.tensor([1, 2], device=DEV)
+
+    def run(s=None):
+        return [M.moe_grouped_gemm(x, o, w, act="gelu", stream=s), M.moe_grouped_gemm_dgrad(dy, o, w, stream=s),
+                M.moe_grouped_gemm_wgrad(dy, o, x, stream=s), M.moe_linear(few, w[0], stream=s),
+                M.moe_dropout(x, 0.4, rng, residual=x, stream=s)]
+
+    ref = run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run(s))
+    torch.cuda.synchronize()
+    for r in got:
+        for a, b in zip(r, ref):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_rows_beyond_31_bits(dt):
     """Elements past 2^31 from the start of x and y: a few rows 2^24 elements apart."""
     g = torch.Generator().manual_seed(8)

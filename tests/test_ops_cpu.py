@@ -104,6 +104,8 @@ BAD_CONFIGS = [
     (dict(groups=0), M.MOE_ERR_INVALID_ARG),
     (dict(groups=257), M.MOE_ERR_UNSUPPORTED),
     (dict(groups=256, n=1 << 23), M.MOE_ERR_UNSUPPORTED),
+    (dict(rows=(1 << 31) - 1024), M.MOE_ERR_UNSUPPORTED),
+    (dict(k=(1 << 31) - 8), M.MOE_ERR_UNSUPPORTED),
     (dict(dtype=2), M.MOE_ERR_INVALID_ARG),
     (dict(ldx=24), M.MOE_ERR_INVALID_ARG),
     (dict(ldx=36), M.MOE_ERR_UNSUPPORTED),
@@ -139,8 +141,9 @@ def test_products_refuse_pointers(L):
     assert forward(L, None) == I
     for name in ("x", "offsets", "w", "y"):
         assert forward(L, cfg, **{name: None}) == I
-    for name in ("x", "w", "bias", "residual", "preact", "y"):
+    for name in ("x", "w", "residual", "preact", "y"):
         assert forward(L, cfg, **{name: PTR + 8}) == U
+    assert forward(L, cfg, bias=PTR + 2) == U
     assert forward(L, cfg, offsets=PTR + 2) == U
     assert forward(L, gcfg(ldr=8), residual=PTR) == I
     assert forward(L, gcfg(ldr=20), residual=PTR) == U
@@ -151,7 +154,7 @@ def test_products_refuse_pointers(L):
     assert L.moe_grouped_gemm_dgrad(cfg, PTR, PTR, PTR, PTR + 4, None, PTR, None, None) == U
     assert L.moe_grouped_gemm_wgrad(cfg, PTR, None, PTR, PTR, None, None, None) == I
     assert L.moe_grouped_gemm_wgrad(cfg, PTR, PTR, None, PTR, None, None, None) == I
-    assert L.moe_grouped_gemm_wgrad(cfg, PTR, PTR, PTR, PTR + 4, None, None, None) == U
+    assert L.moe_grouped_gemm_wgrad(cfg, PTR, PTR, PTR, PTR + 2, None, None, None) == U
     # the dense forms have one group
     assert L.moe_linear(cfg, PTR, PTR, None, None, None, PTR, None, None) == I
     assert L.moe_linear_dgrad(cfg, PTR, PTR, None, None, PTR, None, None) == I
