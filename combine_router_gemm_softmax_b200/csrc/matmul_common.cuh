@@ -60,6 +60,54 @@ MOE_DEV void build_groups(const int32_t* offsets, int E, int rows, int tile_shif
   if (bad && blockIdx.x == 0) report_status(status, MOE_STATUS_BAD_OFFSETS);
 }
 
+// The block of 2^shift rows with index `block`, counted over all groups: its
+// group and rows. False if there are fewer. Every warp finds it for itself
+// (each lane eight groups), so that nothing waits on a barrier before the
+// weights' loads.
+struct RowBlock {
+  int e, r0, end;
+};
+
+MOE_DEV bool find_block(const int32_t* offsets, int E, int rows, int shift, int block, int32_t* status, int lane,
+                        RowBlock& out) {
+  constexpr int kPer = kMaxE / 32;
+  int2 g[kPer];
+  int blocks[kPer], sum = 0;
+  bool bad = false;
+#pragma unroll
+  for (int v = 0; v < kPer; ++v) {
+    const int e = lane * kPer + v;
+    g[v] = e < E ? group_rows(offsets, e, rows, &bad) : make_int2(0, 0);
+    blocks[v] = (g[v].y - g[v].x + (1 << shift) - 1) >> shift;
+    sum += blocks[v];
+  }
+  if (bad) report_status(status, MOE_STATUS_BAD_OFFSETS);
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  const uint32_t past = __ballot_sync(0xffffffffu, inc > block);
+  if (past == 0) return false;
+  int left = block - (inc - sum);  // blocks before it in this lane's groups (if it is this lane's)
+  RowBlock mine{};
+  bool found = false;
+#pragma unroll
+  for (int v = 0; v < kPer; ++v) {
+    if (!found && left < blocks[v]) {
+      mine = {lane * kPer + v, g[v].x + (left << shift), g[v].y};
+      found = true;
+    }
+    left -= blocks[v];
+  }
+  const int src = __ffs(past) - 1;
+  out.e = __shfl_sync(0xffffffffu, mine.e, src);
+  out.r0 = __shfl_sync(0xffffffffu, mine.r0, src);
+  out.end = __shfl_sync(0xffffffffu, mine.end, src);
+  return true;
+}
+
 // The group that row tile t belongs to: prefix[e] <= t < prefix[e+1].
 MOE_DEV int group_of_tile(const int* prefix, int E, int t) {
   int lo = 0, hi = E;

@@ -55,22 +55,16 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) matmul_rows_kernel(c
   constexpr int kThreads = 32 * kWarps;
   constexpr int kFeatures = 16 * kTiles;
   constexpr int kUnroll = 8 / kTiles;  // chunks in flight
-  __shared__ int2 s_rows[kMaxE];
-  __shared__ int prefix[kMaxE + 1];
   __shared__ float s_sum[kWarps][8][kFeatures + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  int e = 0, r0 = blockIdx.y * 8, end = a.rows;
-  if (a.offsets != nullptr) {
-    if (warp == 0) build_groups(a.offsets, a.groups, a.rows, 3, s_rows, prefix, blockIdx.y == 0 ? a.status : nullptr, lane);
-    __syncthreads();
-    const int tile = blockIdx.y;
-    if (tile >= prefix[a.groups]) return;
-    e = group_of_tile(prefix, a.groups, tile);
-    r0 = s_rows[e].x + (tile - prefix[e]) * 8;
-    end = s_rows[e].y;
-  }
-  const int have = min(8, end - r0);
+  RowBlock at{0, static_cast<int>(blockIdx.y) * 8, a.rows};
+  if (a.offsets != nullptr &&
+      !find_block(a.offsets, a.groups, a.rows, 3, blockIdx.y, (blockIdx.x | blockIdx.y | warp) == 0 ? a.status : nullptr,
+                  lane, at))
+    return;
+  const int e = at.e, r0 = at.r0;
+  const int have = min(8, at.end - r0);
   const int n0 = blockIdx.x * kFeatures;
   const int g = lane >> 2, t = lane & 3;
 
@@ -134,23 +128,16 @@ constexpr int kF32Features = 4, kF32Warps = 8;
 template <int kTokens, bool kVec>
 __global__ void __launch_bounds__(32 * kF32Warps) matmul_rows_f32_kernel(const MatmulArgs a) {
   constexpr int kShift = kTokens == 1 ? 0 : kTokens == 2 ? 1 : 2;
-  __shared__ int2 s_rows[kMaxE];
-  __shared__ int prefix[kMaxE + 1];
   __shared__ float s_sum[kF32Warps][kF32Features * kTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  int e = 0, r0 = blockIdx.y * kTokens, end = a.rows;
-  if (a.offsets != nullptr) {
-    if (warp == 0)
-      build_groups(a.offsets, a.groups, a.rows, kShift, s_rows, prefix, blockIdx.y == 0 ? a.status : nullptr, lane);
-    __syncthreads();
-    const int tile = blockIdx.y;
-    if (tile >= prefix[a.groups]) return;
-    e = group_of_tile(prefix, a.groups, tile);
-    r0 = s_rows[e].x + (tile - prefix[e]) * kTokens;
-    end = s_rows[e].y;
-  }
-  const int have = min(kTokens, end - r0), n0 = blockIdx.x * kF32Features;
+  RowBlock at{0, static_cast<int>(blockIdx.y) * kTokens, a.rows};
+  if (a.offsets != nullptr &&
+      !find_block(a.offsets, a.groups, a.rows, kShift, blockIdx.y,
+                  (blockIdx.x | blockIdx.y | warp) == 0 ? a.status : nullptr, lane, at))
+    return;
+  const int e = at.e, r0 = at.r0;
+  const int have = min(kTokens, at.end - r0), n0 = blockIdx.x * kF32Features;
   const float* w = static_cast<const float*>(a.b) + e * a.b_stride + n0 * a.ldb;
   const float* x = static_cast<const float*>(a.a) + static_cast<long long>(r0) * a.lda;
   float acc[kF32Features][kTokens] = {};

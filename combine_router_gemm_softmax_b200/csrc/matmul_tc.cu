@@ -78,7 +78,7 @@ struct TcArgs {
   int n_tiles, m_tiles;  // column tiles; weight mode: row tiles of one group
   int band;              // row tiles per band of the tile walk
   int stall;             // testing hook: the MMA warp first waits on a barrier that nothing signals
-  int align_d, align_p;  // bytes that rows of D and preact start on: 32, 16, or less
+  int align_d, align_p, align_z, align_r;  // bytes that rows of D, preact, z and the residual start on: 32, 16, or less
 };
 
 // full, empty, tails and zeroed per stage, two accumulators' full and empty, the drain; even
@@ -146,10 +146,22 @@ struct Row32 {
   uint4 q[4];
 };
 
-MOE_DEV Row32 load_row(const void* base, long long at, int n0, int n, bool valid) {
+MOE_DEV Row32 load_row(const void* base, long long at, int n0, int n, int align, bool valid) {
   Row32 r;
   const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + at;
-  if (n0 + 32 <= n) {
+  if (n0 + 32 <= n && align >= 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.q[i] = make_uint4(0, 0, 0, 0);
+    if (valid) {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.q[i].x), "=r"(r.q[i].y), "=r"(r.q[i].z), "=r"(r.q[i].w), "=r"(r.q[i + 1].x),
+                       "=r"(r.q[i + 1].y), "=r"(r.q[i + 1].z), "=r"(r.q[i + 1].w)
+                     : "l"(p + 8 * i)
+                     : "memory");
+    }
+  } else if (n0 + 32 <= n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.q[i] = valid ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
   } else {
@@ -235,9 +247,10 @@ MOE_DEV void store_block(uint8_t* stg, const float (&f)[32], float* out, long lo
 // What the epilogue of a rows-mode block reads besides the sums, loaded ahead
 // of them: z (dgrad, if any) or else the residual.
 template <bool kDgrad>
-MOE_DEV Row32 load_ahead(const MatmulArgs& p, long long r, int n0, bool valid) {
-  if (kDgrad && p.z != nullptr) return load_row(p.z, r * p.ldz + n0, n0, p.n, valid);
-  if (p.residual != nullptr) return load_row(p.residual, r * p.ldr + n0, n0, p.n, valid);
+MOE_DEV Row32 load_ahead(const TcArgs& a, long long r, int n0, bool valid) {
+  const MatmulArgs& p = a.p;
+  if (kDgrad && p.z != nullptr) return load_row(p.z, r * p.ldz + n0, n0, p.n, a.align_z, valid);
+  if (p.residual != nullptr) return load_row(p.residual, r * p.ldr + n0, n0, p.n, a.align_r, valid);
   return Row32{};
 }
 
@@ -275,7 +288,7 @@ MOE_DEV void finish_rows(const TcArgs& a, float (&f)[32], const Row32& ahead, in
   }
   if (p.residual != nullptr) {
     const Row32 res = kDgrad && p.z != nullptr
-                          ? load_row(p.residual, r * p.ldr + n0, n0, p.n, valid)
+                          ? load_row(p.residual, r * p.ldr + n0, n0, p.n, a.align_r, valid)
                           : ahead;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -678,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         constexpr bool kDgrad = kMode == MatmulMode::kDgrad, kAhead = !kSplit && !S::kWeight;
         Row32 next{};
-        if constexpr (kAhead) next = load_ahead<kDgrad>(p, row0 + lane, c.n * a.bn + b_first * 32, lane < left);
+        if constexpr (kAhead) next = load_ahead<kDgrad>(a, row0 + lane, c.n * a.bn + b_first * 32, lane < left);
         if (!wait_acc()) break;
         const uint32_t tbase = tmem + (filled & 1) * kBN + lanes;
 #pragma unroll 1
@@ -689,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float f[32];
           tmem_ld32(tbase + c32 * 32, v);
           const Row32 ahead = next;
-          if constexpr (kAhead) next = load_ahead<kDgrad>(p, row0 + lane, n0 + 32, c32 + 1 < b_end && lane < left);
+          if constexpr (kAhead) next = load_ahead<kDgrad>(a, row0 + lane, n0 + 32, c32 + 1 < b_end && lane < left);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
@@ -719,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t row = smem_addr(smem) + b * 4096 + lane * 128;
         Row32 ahead{};
         if constexpr (!S::kWeight)
-          ahead = load_ahead<kMode == MatmulMode::kDgrad>(p, row0 + lane, n0, lane < left);
+          ahead = load_ahead<kMode == MatmulMode::kDgrad>(a, row0 + lane, n0, lane < left);
         float f[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] = 0.0f;
@@ -890,6 +903,8 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   };
   t.align_d = align_of(a.d, a.ldd);
   t.align_p = align_of(a.preact, a.ldz);
+  t.align_z = align_of(a.z, a.ldz);
+  t.align_r = align_of(a.residual, a.ldr);
   bool ok;
   if constexpr (S::kWeight) {
     t.band = 16;
