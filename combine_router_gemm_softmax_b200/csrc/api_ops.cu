@@ -44,7 +44,10 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   p.rc = MOE_ERR_UNSUPPORTED;
   // row and column indices stay below 2^31, a tile past the last one included
   constexpr int32_t kMost = INT32_MAX - 1024;
-  if (c.rows > kMost || c.n > kMost || c.k > kMost) return p;
+  // and the tensor-core tiles' bounded waits last for a bf16 reduction of 2^26 (0.4 s)
+  constexpr int32_t kMostBf16 = 1 << 26;
+  const int32_t most = c.dtype == MOE_DTYPE_BF16 ? kMostBf16 : kMost;
+  if (c.rows > kMost || c.n > most || c.k > most) return p;
   if (c.groups > MOE_MAX_E || static_cast<int64_t>(c.groups) * c.n >= (1LL << 31)) return p;
   if (c.ldx == 0) c.ldx = c.k;
   if (c.ldw == 0) c.ldw = c.k;
@@ -63,8 +66,8 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
     if (c.groups > 1 && !stride_ok(c.w_stride, (c.n - 1) * c.ldw + c.k, bf16, p.rc)) return p;
   }
   // tensor maps hold strides of up to 2^40 bytes
-  const int64_t most = 1LL << 36;
-  if (c.ldx > most || c.ldw > most || c.ldy > most || c.ldr > most || c.ldz > most || c.w_stride > most)
+  const int64_t far = 1LL << 36;
+  if (c.ldx > far || c.ldw > far || c.ldy > far || c.ldr > far || c.ldz > far || c.w_stride > far)
     p.rc = MOE_ERR_UNSUPPORTED;
   return p;
 }
@@ -229,18 +232,19 @@ int32_t moe_dropout(int32_t rows, int32_t cols, int32_t dtype, const void* x, in
 int32_t moe_unpermute_combine_dropout(const moe_config* cfg, const void* y_perm, const int32_t* dest_row,
                                       const float* topk_gate, const void* residual, double p, const uint64_t* rng,
                                       uint64_t offset, void* y, moe_stream_t stream) {
-  if (moe_workspace_size(cfg, MOE_OP_PERMUTE) == 0 && (cfg == nullptr || cfg->T != 0)) {
-    // a rejected configuration: the same code as the plain combine's
-    return moe_unpermute_combine(cfg, y_perm, dest_row, topk_gate, y, nullptr, stream);
-  }
+  int32_t tiles;
+  const int rc = moe_gemm_tiles_used(cfg, &tiles);  // the layer's configuration check
+  if (rc != MOE_OK) return rc;
   DropoutArgs d{};
   if (!dropout_args(p, rng, offset, &d)) return MOE_ERR_INVALID_ARG;
   if (cfg->T > 0 && (!y_perm || !dest_row || !topk_gate || !y)) return MOE_ERR_INVALID_ARG;
   if (!aligned(y_perm, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(dest_row, 4) ||
       !aligned(topk_gate, 4) || !aligned(rng, 8))
     return MOE_ERR_UNSUPPORTED;
-  return rc_of(launch_combine_dropout(cfg->dtype, y_perm, dest_row, topk_gate, residual, d, y, cfg->T, cfg->k, cfg->d,
-                                      static_cast<cudaStream_t>(stream)));
+  const int64_t rows = cfg->layout == MOE_LAYOUT_PADDED ? static_cast<int64_t>(cfg->E) * cfg->capacity
+                                                         : static_cast<int64_t>(cfg->T) * cfg->k;
+  return rc_of(launch_combine_dropout(cfg->dtype, y_perm, static_cast<int>(rows), dest_row, topk_gate, residual, d, y,
+                                      cfg->T, cfg->k, cfg->d, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

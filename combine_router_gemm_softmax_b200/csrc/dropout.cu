@@ -251,8 +251,8 @@ MOE_DEV void combine_token(const uint4* __restrict__ y_perm, const int (&dst)[K]
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads, 3)
     combine_dropout_kernel(const uint4* __restrict__ y_perm, const int32_t* __restrict__ dest_row,
-                           const float* __restrict__ gate, const uint4* residual, uint4* y, int tokens, int vpr,
-                           const DropoutArgs d) {
+                           const float* __restrict__ gate, const uint4* residual, uint4* y, int tokens, int rows,
+                           int vpr, const DropoutArgs d) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
   DropoutState s{};
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < tokens; t += gridDim.x * (kThreads / 32)) {
     const int my_dest = lane < K ? dest_row[static_cast<size_t>(t) * K + lane] : -1;
     const float my_gate = lane < K ? gate[static_cast<size_t>(t) * K + lane] : 0.f;
-    uint32_t rest = __ballot_sync(0xffffffffu, my_dest >= 0);
+    uint32_t rest = __ballot_sync(0xffffffffu, my_dest >= 0 && my_dest < rows);
     const int kept = __popc(rest);
     int dst[K];
     float g[K];
@@ -297,27 +297,27 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 template <typename T, int K>
 cudaError_t launch_combine_k(const uint4* y_perm, const int32_t* dest_row, const float* gate, const uint4* residual,
-                             uint4* y, int tokens, int k, int vpr, const DropoutArgs& d, cudaStream_t s) {
+                             uint4* y, int tokens, int rows, int k, int vpr, const DropoutArgs& d, cudaStream_t s) {
   if constexpr (K < kMaxK) {
-    if (k > K) return launch_combine_k<T, K + 1>(y_perm, dest_row, gate, residual, y, tokens, k, vpr, d, s);
+    if (k > K) return launch_combine_k<T, K + 1>(y_perm, dest_row, gate, residual, y, tokens, rows, k, vpr, d, s);
   }
   const long long grid = std::min<long long>((tokens + 7LL) / 8, device_sm_count() * 8LL);
   return launch_kernel(combine_dropout_kernel<T, K>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, true, 1,
-                       y_perm, dest_row, gate, residual, y, tokens, vpr, d);
+                       y_perm, dest_row, gate, residual, y, tokens, rows, vpr, d);
 }
 
 }  // namespace
 
-cudaError_t launch_combine_dropout(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate,
-                                   const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
+cudaError_t launch_combine_dropout(int dtype, const void* y_perm, int rows, const int32_t* dest_row,
+                                   const float* gate, const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
                                    cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   const uint4* src = static_cast<const uint4*>(y_perm);
   const uint4* res = static_cast<const uint4*>(residual);
   uint4* out = static_cast<uint4*>(y);
   if (dtype == MOE_DTYPE_F32)
-    return launch_combine_k<float, 1>(src, dest_row, gate, res, out, T, k, d / 4, drop, s);
-  return launch_combine_k<__nv_bfloat16, 1>(src, dest_row, gate, res, out, T, k, d / 8, drop, s);
+    return launch_combine_k<float, 1>(src, dest_row, gate, res, out, T, rows, k, d / 4, drop, s);
+  return launch_combine_k<__nv_bfloat16, 1>(src, dest_row, gate, res, out, T, rows, k, d / 8, drop, s);
 }
 
 cudaError_t launch_dropout(int dtype, int rows, int cols, const void* x, long long ldx, const void* residual,

@@ -16,13 +16,13 @@
 // offsets. Warp 0 loads a ring of up to 8 stages (192 KB) by TMA, one thread
 // of warp 1 issues tcgen05.mma into one of two TMEM accumulators, warps 2..9
 // drain the other: bias, activation, slope and residual in fp32, one rounding,
-// a row a thread straight to global memory. Three forms:
+// then stores. Three forms:
 //
 //   kPair    256 x bn tiles on a cluster of two CTAs (cta_group::2): each loads
-//            128 rows of A and half of B, 32 KB a stage at bn = 256, so that
-//            six stages cover 3000 cycles of load latency. The form for large
-//            products.
-//   kSingle  128 x bn tiles, a CTA each (48 KB a stage): groups of few rows,
+//            128 rows of A and half of B, 32 KB for a block of 64 along the
+//            reduction at bn = 256, so that the ring covers 3000 cycles of load
+//            latency. The form for large products.
+//   kSingle  128 x bn tiles, a CTA each (48 KB a block): groups of few rows,
 //            whose 256-row tiles would be padding.
 //   kSplit   a cluster of CTAs shares one 128 x bn tile's reduction when there
 //            are few tiles: the partial tiles lie in the CTAs' own shared
@@ -33,6 +33,11 @@
 // The width bn is chosen per call so that the tiles fill the SMs evenly
 // (choose_tiles); the last column tile issues MMAs only as wide as it is.
 //
+// Bound: the tensor pipe, at the clock that the 1 kW limit leaves (8192 x 4096 x
+// 4096: pipe 91-92% active forward and dgrad, 81% wgrad; 8192 x 14336 x 4096:
+// 1.29-1.37 PFLOP/s in loops, as a library product); for short reductions the
+// epilogue, for few rows a group the weights' bytes.
+//
 // wgrad's reduction is the group's rows: its last 64-row block may run into
 // the next group, so warp 1 zeroes those rows of both operands in shared memory
 // (a row of a tile is 128 contiguous bytes whatever the swizzle) before the MMA
@@ -41,9 +46,10 @@
 // The tensor cores add into an fp32 accumulator by truncation, which biases a
 // long sum towards zero by about 1.1e-9 of it a row (measured: 1.9e-5 over
 // 16384 rows). bf16 outputs do not notice; wgrad's fp32 ones would. So wgrad
-// keeps an accumulator for kChainBlocks blocks (512 rows: 4.7e-7) only and the
+// keeps an accumulator for kChainBlocks blocks (768 rows: 7e-7) only and the
 // epilogue adds these partial sums, rounded to nearest, in registers, while
-// the MMAs fill the other accumulator.
+// the MMAs fill the other accumulator (8192 rows, 4096 x 14336: 702 us; 512
+// rows an accumulator 718, all rows in one 682).
 #include <cmath>
 
 #include "matmul_common.cuh"
@@ -57,7 +63,7 @@ constexpr int kBK = 64;
 constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kChainBlocks = 8;  // wgrad: blocks of the reduction added in one accumulator
+constexpr int kChainBlocks = 12;  // wgrad: blocks of the reduction added in one accumulator
 constexpr uint32_t kABytes = kBM * kBK * 2;  // one CTA's rows of A
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements

@@ -173,8 +173,9 @@ struct DropoutArgs {
 // dropout.cu
 cudaError_t launch_dropout(int dtype, int rows, int cols, const void* x, long long ldx, const void* residual,
                            long long ldr, void* y, long long ldy, const DropoutArgs& d, cudaStream_t s);
-cudaError_t launch_combine_dropout(int dtype, const void* y_perm, const int32_t* dest_row, const float* gate,
-                                   const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
+// rows: of y_perm; a destination outside them counts as dropped.
+cudaError_t launch_combine_dropout(int dtype, const void* y_perm, int rows, const int32_t* dest_row,
+                                   const float* gate, const void* residual, const DropoutArgs& drop, void* y, int T, int k, int d,
                                    cudaStream_t s);
 
 // The free products (matmul_common.cuh describes the modes). Strides in elements.

@@ -446,7 +446,7 @@ MOE_API int32_t moe_debug_stall_next_gemms(int32_t n);
  * ones on tensor cores. No workspace. Deterministic.
  * No other operand may overlap an output.
  * Limits: 1 <= groups <= MOE_MAX_E, n, k >= 1, n * groups < 2^31, rows, n and
- * k at most 2^31 - 1025.
+ * k at most 2^31 - 1025 (bf16: n and k at most 2^26).
  * Errors: MOE_ERR_INVALID_ARG (NULL, negative sizes, a stride below its
  * width, unknown act or dtype), MOE_ERR_UNSUPPORTED (limits, a pointer off 16
  * bytes (bias, dw, dbias, offsets: 4), a bf16 stride that is no multiple of
@@ -515,7 +515,8 @@ MOE_API int32_t moe_dropout(int32_t rows, int32_t cols, int32_t dtype, const voi
  * moe_unpermute_combine's sum (fp32, not rounded in between), moe_dropout's
  * mask on it (rows t, columns of d) and the residual stream added:
  *   y[t] = residual[t] + dropout(sum_j topk_gate[t, j] y_perm[dest_row[t, j]])
- * residual [T, d] (dtype) or NULL; it may be y. The gradient that enters
+ * residual [T, d] (dtype) or NULL; it may be y. A destination outside y_perm's
+ * rows counts as dropped. The gradient that enters
  * moe_layer_backward is moe_dropout(dy) with the same p, rng and offset. */
 MOE_API int32_t moe_unpermute_combine_dropout(const moe_config* cfg, const void* y_perm, const int32_t* dest_row,
                                               const float* topk_gate, const void* residual, double p,

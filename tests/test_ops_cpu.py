@@ -106,6 +106,8 @@ BAD_CONFIGS = [
     (dict(groups=256, n=1 << 23), M.MOE_ERR_UNSUPPORTED),
     (dict(rows=(1 << 31) - 1024), M.MOE_ERR_UNSUPPORTED),
     (dict(k=(1 << 31) - 8), M.MOE_ERR_UNSUPPORTED),
+    (dict(k=(1 << 26) + 8), M.MOE_ERR_UNSUPPORTED),
+    (dict(n=(1 << 26) + 8, groups=1), M.MOE_ERR_UNSUPPORTED),
     (dict(dtype=2), M.MOE_ERR_INVALID_ARG),
     (dict(ldx=24), M.MOE_ERR_INVALID_ARG),
     (dict(ldx=36), M.MOE_ERR_UNSUPPORTED),
@@ -209,6 +211,7 @@ def test_combine_dropout_refuses(L):
     assert call(cfg=None) == I
     assert call(cfg=M.config(8, 96, 4, 2, 128)) == U
     assert call(cfg=M.config(8, 128, 4, 5, 128)) == U
+    assert call(cfg=M.config(0, 96, 4, 2, 128)) == U
     for name in ("y_perm", "dest", "gate", "y"):
         assert call(**{name: None}) == I
     assert call(p=1.0) == I and call(p=1.5) == I and call(rng=None) == I
