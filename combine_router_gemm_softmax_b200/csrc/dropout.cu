@@ -4,7 +4,7 @@
 // Bound: HBM (x and the residual read, y written, once each), with the
 // generator's integer work close behind: a thread keeps one column of 16-byte
 // vectors and walks down its rows, so that what the generator does to the
-// column is done once (18 instead of 23 multiplies a block of four words), and
+// column is done once (15 instead of 20 products a block of four words), and
 // starts the loads of several rows before it draws any word.
 #include "dropout.cuh"
 

@@ -3,10 +3,10 @@
 //
 // Bound: HBM, the weights of the groups that have rows, each read once. A
 // 128-row tile would leave most of its rows empty and, with one CTA a tile,
-// too few SMs with loads in flight. Here a CTA of 8 warps takes 32 output
-// features (16 where that would be few CTAs) of one group and 8 of its rows; its warps share the
-// reduction, and their sums meet in shared memory in warp order (the same
-// result on every run).
+// too few SMs with loads in flight. Here a CTA of 8 or 4 warps takes 16 or 32
+// output features of one group and 8 of its rows (launch_matmul_rows has the
+// rule); its warps share the reduction, and their sums meet in shared memory in
+// warp order (the same result on every run).
 //
 // The weights go from global memory straight into the fragments of mma.sync
 // (m16n8k16, W as the 16-row operand, the tokens as the 8 columns): a lane

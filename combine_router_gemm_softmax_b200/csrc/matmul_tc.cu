@@ -34,9 +34,10 @@
 // (choose_tiles); the last column tile issues MMAs only as wide as it is.
 //
 // Bound: the tensor pipe, at the clock that the 1 kW limit leaves (8192 x 4096 x
-// 4096: pipe 91-92% active forward and dgrad, 81% wgrad; 8192 x 14336 x 4096:
-// 1.29-1.37 PFLOP/s in loops, as a library product); for short reductions the
-// epilogue, for few rows a group the weights' bytes.
+// 4096: pipe 91-92% active forward and dgrad, 81% wgrad with 512-row
+// accumulators; 8192 x 14336 x 4096 forward and dgrad: 1.27-1.35 PFLOP/s in
+// loops, a library product 1.32-1.37); for short reductions the epilogue, for
+// few rows a group the weights' bytes.
 //
 // wgrad's reduction is the group's rows: its last 64-row block may run into
 // the next group, so warp 1 zeroes those rows of both operands in shared memory
