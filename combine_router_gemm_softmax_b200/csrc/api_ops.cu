@@ -148,7 +148,8 @@ int wgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
     if (rc != MOE_OK) return rc;
   }
   if (dbias)
-    return rc_of(launch_column_sums(c.dtype, dy, c.ldy, offsets, c.groups, c.rows, c.n, dbias, c.n % 4 == 0 && c.ldy % 4 == 0, s));
+    return rc_of(launch_column_sums(c.dtype, dy, c.ldy, offsets, c.groups, c.rows, c.n, dbias, dw ? nullptr : status,
+                                    c.n % 4 == 0 && c.ldy % 4 == 0, s));
   return MOE_OK;
 }
 

@@ -327,14 +327,17 @@ cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t
 // columns (four a lane) and every 16th row, eight rows in flight each (two
 // CTAs an SM; 16 rows in flight leave room for one, and 134 MB took 79 us
 // instead of 31); the cluster's CTAs share the rows, and their sums meet in
-// distributed shared memory in rank order. Bound: HBM (dy read once).
+// distributed shared memory in rank order. Bound: HBM (dy read once). status
+// (or NULL, when a product of the same call looks the offsets over) receives
+// MOE_STATUS_BAD_OFFSETS from the first CTA's first warp.
 namespace {
 
 constexpr int kSumWarps = 16, kSumRows = 8;
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const T* dy, long long ld, const int32_t* offsets,
-                                                                    int rows, int n, float* out) {
+                                                                    int rows, int n, float* out, int groups,
+                                                                    int32_t* status) {
   __shared__ __align__(16) float s_sum[kSumWarps][128];
   uint32_t split, part;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
@@ -342,6 +345,11 @@ __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const T* dy,
   const int e = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n0 = static_cast<int>(blockIdx.x / split) * 128;
   pdl_wait();
+  if (status != nullptr && (blockIdx.x | blockIdx.y | warp) == 0) {
+    bool bad = false;
+    for (int i = lane; i < groups; i += 32) group_rows(offsets, i, rows, &bad);
+    if (bad) report_status(status, MOE_STATUS_BAD_OFFSETS);
+  }
   const int2 g = group_rows(offsets, e, rows);
   const long long have = g.y - g.x;
   const int r0 = g.x + static_cast<int>(have * part / split), r1 = g.x + static_cast<int>(have * (part + 1) / split);
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const T* dy,
 
 template <typename T>
 cudaError_t column_sums(const void* dy, long long ld, const int32_t* offsets, int groups, int rows, int n, float* out,
-                        bool vec, cudaStream_t s) {
+                        int32_t* status, bool vec, cudaStream_t s) {
   const int blocks = (n + 127) / 128;
   int split = 1;
   while (split < 8 && static_cast<long long>(blocks) * groups * split * 2 <= 2LL * device_sm_count() &&
@@ -385,7 +393,7 @@ cudaError_t column_sums(const void* dy, long long ld, const int32_t* offsets, in
     split *= 2;
   return launch_kernel(vec ? column_sum_kernel<T, true> : column_sum_kernel<T, false>, dim3(blocks * split, groups),
                        dim3(32 * kSumWarps), 0, s, true, static_cast<unsigned>(split), static_cast<const T*>(dy), ld,
-                       offsets, rows, n, out);
+                       offsets, rows, n, out, groups, status);
 }
 
 // dz = dy act'(z), elementwise over [rows, n], four columns a step. Bound: HBM.
@@ -431,9 +439,9 @@ cudaError_t act_backward(const void* dy, long long ldy, const void* z, long long
 }  // namespace
 
 cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const int32_t* offsets, int groups, int rows,
-                               int n, float* out, bool vec, cudaStream_t s) {
-  return dtype == MOE_DTYPE_F32 ? column_sums<float>(dy, ld, offsets, groups, rows, n, out, vec, s)
-                                : column_sums<__nv_bfloat16>(dy, ld, offsets, groups, rows, n, out, vec, s);
+                               int n, float* out, int32_t* status, bool vec, cudaStream_t s) {
+  return dtype == MOE_DTYPE_F32 ? column_sums<float>(dy, ld, offsets, groups, rows, n, out, status, vec, s)
+                                : column_sums<__nv_bfloat16>(dy, ld, offsets, groups, rows, n, out, status, vec, s);
 }
 
 cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const void* z, long long ldz, void* dz,

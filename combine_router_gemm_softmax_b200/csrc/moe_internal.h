@@ -206,9 +206,9 @@ bool matmul_few_rows_f32(const MatmulArgs& a);
 cudaError_t launch_matmul_rows_f32(const MatmulArgs& a, cudaStream_t s);
 // matmul_tc.cu (strides and addresses on 16 bytes)
 cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
-// matmul_simt.cu
+// matmul_simt.cu; status: NULL if a product of the same call reports the offsets
 cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const int32_t* offsets, int groups, int rows,
-                               int n, float* out, bool vec, cudaStream_t s);
+                               int n, float* out, int32_t* status, bool vec, cudaStream_t s);
 cudaError_t launch_act_backward(int dtype, const void* dy, long long ldy, const void* z, long long ldz, void* dz,
                                 long long ldd, int rows, int n, int act, bool vec, cudaStream_t s);
 
