@@ -183,7 +183,10 @@ extern "C" {
 
 /* Activations of the free products (moe_grouped_gemm, moe_linear): the
  * identity, max(z, 0), z Phi(z) (Phi the normal distribution function),
- * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2, and z / (1 + e^-z). */
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2, and z / (1 + e^-z). They
+ * are evaluated in fp32, for bf16 matrices with fast exponentials and
+ * reciprocals: within 3e-5 of their value, far negative z included, down to
+ * values of 1e-36, below which they may come out as zero. */
 #define MOE_ACT_NONE      0
 #define MOE_ACT_RELU      1
 #define MOE_ACT_GELU      2

@@ -38,3 +38,32 @@ def test_bias_gradient_alone_reports_bad_offsets(dt, off, bad):
     if not bad:
         want = torch.stack([dy[a:b].float().sum(0) for _, (a, b) in R.groups(off)])
         assert torch.equal(db, want)
+
+
+def far_act(u, name):
+    """The activations in 64 bits without cancellation far out (1 + tanh loses its digits from -6 on)."""
+    c = math.sqrt(2 / math.pi)
+    return {"gelu": lambda: u * 0.5 * torch.special.erfc(-u / math.sqrt(2)), "silu": lambda: u * torch.sigmoid(u),
+            "gelu_tanh": lambda: u * torch.sigmoid(2 * c * (u + 0.044715 * u ** 3))}[name]()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("act,least", [("gelu", -12.75), ("gelu_tanh", -9.5), ("silu", -80.0)])
+def test_negative_tails_keep_their_digits(dt, act, least):
+    """Activations and slopes against their own small values, down to `least` (the values stay above 1e-36, inside
+    the types' normal range). Relative errors: half a step of the type, and the evaluation's, whose largest part is
+    the exponent: up to 125 in base 2, five roundings of 2^-24 of it at most, times ln 2: 2.6e-5 with GELU's tanh
+    form, less with the others; 3e-5 with the function's own error. A slope is the sum of two such terms; where it
+    is tested it is at least 0.43 of the larger one, so its bound is three times that."""
+    u = torch.cat([torch.linspace(least, -2.0, 250), torch.linspace(2.0, 12.0, 150)]).to(dt).reshape(25, 16).to(DEV)
+    ud = u.cpu().double().requires_grad_()
+    want = far_act(ud, act)
+    slope, = torch.autograd.grad(want.sum(), ud)
+    want = want.detach()
+    half = torch.finfo(dt).eps / 2
+    eye = torch.eye(16, dtype=dt, device=DEV)
+    for name, got, ref, err in (("rows", M.moe_linear(u[:8], eye, act=act), want[:8], 3e-5),
+                                ("tiles", M.moe_linear(u.repeat(300, 1), eye, act=act)[-25:], want, 3e-5),
+                                ("slope", M.moe_act_backward(torch.ones_like(u), u, act), slope, 9e-5)):
+        off = (got.cpu().double() - ref).abs() / ref.abs()
+        assert float(off.max()) <= half + err, (name, float(off.max()), float(u.cpu().reshape(-1)[int(off.argmax())]))
