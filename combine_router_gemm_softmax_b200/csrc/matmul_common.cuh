@@ -213,7 +213,8 @@ MOE_DEV float slope_value(float z) {
     return fmaf(z * 0.3989422804014327f, gauss, phi);
   } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
     const float s = gelu_sigmoid<kFast>(z);
-    const float du = fmaf(z * z, 6.0f * kGeluTanhC * kGeluTanhA, 2.0f * kGeluTanhC);
+    // far out s - s^2 is zero, and stays zero times a finite du
+    const float du = fmaf(fminf(z * z, 1e30f), 6.0f * kGeluTanhC * kGeluTanhA, 2.0f * kGeluTanhC);
     return fmaf(z * fmaf(-s, s, s), du, s);
   } else if constexpr (kAct == MOE_ACT_SILU) {
     const float s = sigmoid_of<kFast>(z);

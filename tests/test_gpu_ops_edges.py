@@ -67,3 +67,20 @@ def test_negative_tails_keep_their_digits(dt, act, least):
                                 ("slope", M.moe_act_backward(torch.ones_like(u), u, act), slope, 9e-5)):
         off = (got.cpu().double() - ref).abs() / ref.abs()
         assert float(off.max()) <= half + err, (name, float(off.max()), float(u.cpu().reshape(-1)[int(off.argmax())]))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("act", R.ACTS)
+def test_activations_far_from_zero(act, dt):
+    """Any finite argument: past 100 every activation is its argument or zero and its slope one or zero, exactly,
+    up to the largest numbers of the type (whose squares and cubes are infinite), and NaN stays in its place."""
+    big = [100.0, 1e10, 1.8e19, 2e19, 1e20, 1e38, torch.finfo(dt).max]
+    z = torch.tensor([big + [-v for v in big] + [math.nan, 0.0]], device=DEV).to(dt)
+    ones = torch.ones_like(z)
+    pos = torch.cat([torch.ones(7), torch.full((7,), 1.0 if act == "none" else 0.0)]).to(dt)
+    slopes = [M.moe_act_backward(ones, z, act), M.moe_linear_dgrad(ones, torch.eye(16, device=DEV).to(dt), z=z, act=act)]
+    for got in slopes:
+        assert torch.equal(got[0, :14].cpu(), pos)
+        assert act == "relu" or act == "none" or bool(got[0, 14].isnan())
+    v = M.moe_linear(torch.nan_to_num(z, nan=0.0), torch.eye(16, device=DEV).to(dt), act=act)[0, :14].cpu()
+    assert torch.equal(v, pos * z[0, :14].cpu())
