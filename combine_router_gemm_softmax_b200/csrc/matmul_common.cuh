@@ -162,29 +162,56 @@ MOE_DEV float gelu_sigmoid(float z) {
   }
 }
 
-// Phi, the standard normal distribution function, and gauss = exp(-z^2 / 2).
-// Fast: Phi(-|z|) = gauss s q(s) with s = 1 / (1 + 0.3086339 |z|) and q of
-// degree five, fitted for the least relative error of Phi(-|z|) over
-// |z| <= 14.5: 4.1e-6, about 1e-5 with the rounding of z^2 / 2, so that GELU's
-// negative tail keeps its bf16 digits down to where gauss leaves fp32's normal
-// range (z < -13.2: zero, true values below 1e-37). Else erfc itself, which
-// keeps its relative precision in the negative tail.
+// The negative tail of Phi, the standard normal distribution function, by fast
+// instructions: Phi(-|z|) = gauss s q(s) with gauss = exp(-z^2 / 2),
+// s = 1 / (1 + 0.3086339 |z|) and q of degree five, fitted for the least
+// relative error of Phi(-|z|) over |z| <= 14.5: 4.1e-6, about 1e-5 with the
+// rounding of z^2 / 2. So GELU keeps its bf16 digits down to where gauss
+// leaves fp32's normal range (z < -13.2: zero, true values below 1e-37).
+struct FastTail {
+  float s, q, gauss;
+};
+
+MOE_DEV FastTail fast_tail(float z, float abs_z) {
+  FastTail t;
+  t.s = rcp_fast(fmaf(0.30863391f, abs_z, 1.0f));
+  t.gauss = ex2_fast(z * z * (-0.5f * kLog2E));
+  t.q = fmaf(-0.07501083f, t.s, 0.18683868f);
+  t.q = fmaf(t.q, t.s, 0.00985154f);
+  t.q = fmaf(t.q, t.s, 0.13559357f);
+  t.q = fmaf(t.q, t.s, 0.11936795f);
+  t.q = fmaf(t.q, t.s, 0.12335706f);
+  return t;
+}
+
+// z Phi(z). Fast: max(z, 0) - |z| Phi(-|z|), which needs no choice by sign;
+// |z| is held to 15, where gauss is zero, so that infinity meets no zero.
+// Else erfc, which keeps its relative precision in the negative tail.
 template <bool kFast>
-MOE_DEV float phi_of(float z, float& gauss) {
+MOE_DEV float gelu_of(float z) {
   if constexpr (kFast) {
-    const float s = rcp_fast(fmaf(0.30863391f, fabsf(z), 1.0f));
-    gauss = ex2_fast(z * z * (-0.5f * kLog2E));
-    float p = fmaf(-0.07501083f, s, 0.18683868f);
-    p = fmaf(p, s, 0.00985154f);
-    p = fmaf(p, s, 0.13559357f);
-    p = fmaf(p, s, 0.11936795f);
-    p = fmaf(p, s, 0.12335706f);
-    const float tail = p * s * gauss;  // Phi(-|z|)
-    return z < 0.0f ? tail : 1.0f - tail;
+    const float abs_z = fminf(fabsf(z), 15.0f);
+    const FastTail t = fast_tail(z, abs_z);
+    return fmaf(-(abs_z * t.s * t.gauss), t.q, fmaxf(z, 0.0f));
+  } else {
+    return z * (0.5f * erfcf(-z * 0.70710678118654752f));
+  }
+}
+
+// Phi(z) + z gauss / sqrt(2 pi), the slope of it.
+template <bool kFast>
+MOE_DEV float gelu_slope(float z) {
+  float phi, gauss;
+  if constexpr (kFast) {
+    const FastTail t = fast_tail(z, fabsf(z));
+    gauss = t.gauss;
+    const float tail = t.q * t.s * gauss;
+    phi = z < 0.0f ? tail : 1.0f - tail;
   } else {
     gauss = expf(-0.5f * z * z);
-    return 0.5f * erfcf(-z * 0.70710678118654752f);
+    phi = 0.5f * erfcf(-z * 0.70710678118654752f);
   }
+  return fmaf(z * 0.3989422804014327f, gauss, phi);
 }
 
 template <int kAct, bool kFast>
@@ -192,8 +219,7 @@ MOE_DEV float act_value(float z) {
   if constexpr (kAct == MOE_ACT_RELU) {
     return z > 0.0f ? z : (z != z ? z : 0.0f);
   } else if constexpr (kAct == MOE_ACT_GELU) {
-    float gauss;
-    return z * phi_of<kFast>(z, gauss);
+    return gelu_of<kFast>(z);
   } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
     return z * gelu_sigmoid<kFast>(z);
   } else if constexpr (kAct == MOE_ACT_SILU) {
@@ -208,9 +234,7 @@ MOE_DEV float slope_value(float z) {
   if constexpr (kAct == MOE_ACT_RELU) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (kAct == MOE_ACT_GELU) {
-    float gauss;
-    const float phi = phi_of<kFast>(z, gauss);
-    return fmaf(z * 0.3989422804014327f, gauss, phi);
+    return gelu_slope<kFast>(z);
   } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
     const float s = gelu_sigmoid<kFast>(z);
     // far out s - s^2 is zero, and stays zero times a finite du
