@@ -44,7 +44,7 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   p.rc = MOE_ERR_UNSUPPORTED;
   // row and column indices stay below 2^31, a tile past the last one included
   constexpr int32_t kMost = INT32_MAX - 1024;
-  // and the tensor-core tiles' bounded waits last for a bf16 reduction of 2^26 (0.4 s)
+  // and bf16 widths at most what the tensor-core tiles' bounded waits are known to last for
   constexpr int32_t kMostBf16 = 1 << 26;
   const int32_t most = c.dtype == MOE_DTYPE_BF16 ? kMostBf16 : kMost;
   if (c.rows > kMost || c.n > most || c.k > most) return p;

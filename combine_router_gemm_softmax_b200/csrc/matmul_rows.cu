@@ -20,6 +20,11 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 32;  // reduction elements of a step
+// Chunks that a warp adds in one set of accumulators. The tensor cores truncate
+// when they add (6e-5 of a sum of 16384 elements of one sign, 7e-4 of 131072);
+// after 4096 elements the sums go to shared memory and are added there, rounded
+// to nearest. Reductions of up to 16384 never get there.
+constexpr int kChainChunks = 128;
 
 // Eight elements of a row from p: all of them, or the first `valid`, or none.
 template <bool kStream>
@@ -75,36 +80,41 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) matmul_rows_kernel(c
   const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.b) + e * a.b_stride + (n0 + g) * a.ldb + t * 8;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.a) + (static_cast<long long>(r0) + g) * a.lda + t * 8;
   float acc[kTiles][4];
+  // rows g and g + 8 of the 16 features, tokens 2 t and 2 t + 1
+  auto sum_at = [&](int m, int i) -> float& { return s_sum[warp][2 * t + (i & 1)][m * 16 + g + 8 * (i >> 1)]; };
+  int from = c0;
+  do {
+    const int to = min(from + kChainChunks, c1);
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+    for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
-
-  for (int c = c0; c < c1; c += kUnroll) {
-    uint4 qw[kUnroll][2 * kTiles], qx[kUnroll];
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
+    for (int c = from; c < to; c += kUnroll) {
+      uint4 qw[kUnroll][2 * kTiles], qx[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int k = (c + u) * kChunk;
-      const int valid = c + u < c1 ? a.k - k - t * 8 : 0;  // of this lane's eight
+      for (int u = 0; u < kUnroll; ++u) {
+        const int k = (c + u) * kChunk;
+        const int valid = c + u < c1 ? a.k - k - t * 8 : 0;  // of this lane's eight
 #pragma unroll
-      for (int i = 0; i < 2 * kTiles; ++i)
-        qw[u][i] = load8<true>(w + static_cast<long long>(i) * 8 * a.ldb + k, n0 + g + 8 * i < a.n ? valid : 0);
-      qx[u] = load8<false>(x + k, g < have ? valid : 0);
+        for (int i = 0; i < 2 * kTiles; ++i)
+          qw[u][i] = load8<true>(w + static_cast<long long>(i) * 8 * a.ldb + k, n0 + g + 8 * i < a.n ? valid : 0);
+        qx[u] = load8<false>(x + k, g < have ? valid : 0);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const uint4 &lo = qw[u][2 * m], &hi = qw[u][2 * m + 1];
+          mma(acc[m], lo.x, hi.x, lo.y, hi.y, qx[u].x, qx[u].y);
+          mma(acc[m], lo.z, hi.z, lo.w, hi.w, qx[u].z, qx[u].w);
+        }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
+    for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        const uint4 &lo = qw[u][2 * m], &hi = qw[u][2 * m + 1];
-        mma(acc[m], lo.x, hi.x, lo.y, hi.y, qx[u].x, qx[u].y);
-        mma(acc[m], lo.z, hi.z, lo.w, hi.w, qx[u].z, qx[u].w);
-      }
-  }
-  // rows g and g + 8 of the 16 features, tokens 2 t and 2 t + 1
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_sum[warp][2 * t + (i & 1)][m * 16 + g + 8 * (i >> 1)] = acc[m][i];
+      for (int i = 0; i < 4; ++i) sum_at(m, i) = from > c0 ? sum_at(m, i) + acc[m][i] : acc[m][i];
+    from = to;
+  } while (from < c1);
   __syncthreads();
   for (int i = threadIdx.x; i < have * kFeatures; i += kThreads) {
     const int token = i / kFeatures, f = i % kFeatures, n = n0 + f;

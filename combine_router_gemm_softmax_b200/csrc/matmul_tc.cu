@@ -46,11 +46,14 @@
 //
 // The tensor cores add into an fp32 accumulator by truncation, which biases a
 // long sum towards zero by about 1.1e-9 of it a row (measured: 1.9e-5 over
-// 16384 rows). bf16 outputs do not notice; wgrad's fp32 ones would. So wgrad
-// keeps an accumulator for kChainBlocks blocks (768 rows: 7e-7) only and the
-// epilogue adds these partial sums, rounded to nearest, in registers, while
-// the MMAs fill the other accumulator (8192 rows, 4096 x 14336: 702 us; 512
-// rows an accumulator 718, all rows in one 682).
+// 16384 rows, more than in proportion beyond). An accumulator therefore takes
+// chain_blocks() of the reduction only, and the epilogue adds these partial
+// sums, rounded to nearest, in registers, while the MMAs fill the other
+// accumulator. wgrad's fp32 outputs take 768 rows (7e-7; 8192 rows, 4096 x
+// 14336: 702 us; 512 rows an accumulator 718, all rows in one 682), the bf16
+// outputs of the rows modes 16384 elements, a hundredth of half their step, so
+// that no reduction grows less exact than that. In rows mode the adding is an
+// instance of its own (kChained), since its registers spill in the others.
 #include <cmath>
 
 #include "matmul_common.cuh"
@@ -64,7 +67,9 @@ constexpr int kBK = 64;
 constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kChainBlocks = 12;  // wgrad: blocks of the reduction added in one accumulator
+
+// Blocks of the reduction added in one accumulator (whole stages of the ring).
+constexpr int chain_blocks(MatmulMode m) { return m == MatmulMode::kWgrad ? 12 : 256; }
 constexpr uint32_t kABytes = kBM * kBK * 2;  // one CTA's rows of A
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements
@@ -320,13 +325,17 @@ MOE_DEV void finish_block(const TcArgs& a, float (&f)[32], const Row32& ahead, c
   }
 }
 
-template <MatmulMode kMode, Form kForm>
+// kChained: reductions may be longer than an accumulator takes (always, in weight mode).
+template <MatmulMode kMode, Form kForm, bool kChained>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const TcArgs a) {
   using S = Shape<kMode>;
   constexpr bool kPair = kForm == Form::kPair, kSplit = kForm == Form::kSplit;
   constexpr int kTileM = kPair ? 2 * kBM : kBM, kPerStage = blocks_per_stage(kForm);
+  constexpr int kChain = chain_blocks(kMode);
+  static_assert(kChain % kPerStage == 0, "an accumulator takes whole stages");
+  static_assert(kChained || !S::kWeight, "a group may have any number of rows, none too");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);  // the ring: per stage A, then B
   uint8_t* stg_all = smem + S::kRingBytes;
@@ -531,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile c = tile_at(t);
       const uint32_t idesc =
           idesc_bf16_f32(kTileM, width_of(c)) | (S::kAcrossA ? 1u << 15 : 0u) | (S::kAcrossB ? 1u << 16 : 0u);
-      for (int k0 = c.kb0; k0 < c.kb1 && !stop; k0 += S::kWeight ? kChainBlocks : c.kb1 - c.kb0, ++filled) {
+      for (int k0 = c.kb0; k0 < c.kb1 && !stop; k0 += kChained ? kChain : c.kb1 - c.kb0, ++filled) {
         const int acc = filled & 1;
         if (leader || !kPair) {
           if (!mbar_wait(&tempty[acc], ((filled >> 1) & 1) ^ 1, abort_flag)) {
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         const uint32_t d_tmem = tmem + acc * kBN;
-        const int k1 = S::kWeight ? min(k0 + kChainBlocks, c.kb1) : c.kb1;
+        const int k1 = kChained ? min(k0 + kChain, c.kb1) : c.kb1;
         for (int kb = k0; kb < k1; kb += kPerStage) {
           const int blocks = min(kPerStage, k1 - kb);
           const int have = S::kWeight ? rows_in(c, kb + blocks - 1) : kBK;  // of the stage's last block
@@ -662,15 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = c.m * kTileM + (kPair ? static_cast<int>(rank) * kBM : 0) + q * 32;
       const int row0 = S::kWeight ? m0 : c.rows.x + m0;
       const int left = S::kWeight ? p.m - row0 : c.rows.y - row0;  // rows from row0 to the end
-      const bool whole = !S::kWeight || (c.kb1 > c.kb0 && c.kb1 - c.kb0 <= kChainBlocks);  // one accumulator holds the sums
-      if (S::kWeight && !whole) {
+      const bool whole = !kChained || (c.kb1 > c.kb0 && c.kb1 - c.kb0 <= kChain);  // one accumulator holds the sums
+      if (kChained && !whole) {
         float f[4][32];
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[b][i] = 0.0f;
         bool ok = true;
-        for (int k0 = c.kb0; k0 < c.kb1; k0 += kChainBlocks) {
+        for (int k0 = c.kb0; k0 < c.kb1; k0 += kChain) {
           if (!(ok = wait_acc())) break;
           const uint32_t tbase = tmem + (filled & 1) * kBN + lanes + b_first * 32;
 #pragma unroll
@@ -692,7 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kSplit) {
             keep_partial(c32, f[b]);
           } else {
-            if (n0 < p.n && left > 0) finish_block<kMode>(a, f[b], Row32{}, c, row0, left, n0, stg, lane);
+            if (n0 >= p.n || left <= 0) continue;
+            Row32 ahead{};
+            if constexpr (!S::kWeight)
+              ahead = load_ahead<kMode == MatmulMode::kDgrad>(a, row0 + lane, n0, lane < left);
+            finish_block<kMode>(a, f[b], ahead, c, row0, left, n0, stg, lane);
           }
         }
       } else {
@@ -797,16 +810,25 @@ bool load_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, ui
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <MatmulMode kMode, Form kForm>
-cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& t, long long grid, int cluster,
+template <MatmulMode kMode, Form kForm, bool kChained>
+cudaError_t launch_chained(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& t, long long grid, int cluster,
                          cudaStream_t s) {
   using S = Shape<kMode>;
-  auto* kernel = matmul_tc_kernel<kMode, kForm>;
+  auto* kernel = matmul_tc_kernel<kMode, kForm, kChained>;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
   return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, s, true,
                        static_cast<unsigned>(cluster), ta, tb, t);
+}
+
+// blocks: along the reduction, of the CTA that has most of them (rows modes).
+template <MatmulMode kMode, Form kForm>
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& t, int blocks, long long grid,
+                         int cluster, cudaStream_t s) {
+  if constexpr (!Shape<kMode>::kWeight)
+    if (blocks <= chain_blocks(kMode)) return launch_chained<kMode, kForm, false>(ta, tb, t, grid, cluster, s);
+  return launch_chained<kMode, kForm, true>(ta, tb, t, grid, cluster, s);
 }
 
 // How a product is cut up.
@@ -930,11 +952,12 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
   if (tiles >= 1LL << 31) return cudaErrorInvalidValue;
   switch (choice.form) {
     case Form::kPair:
-      return launch_tiles<kMode, Form::kPair>(ta, tb, t, 2 * std::min<long long>(tiles, sms / 2), 2, s);
+      return launch_tiles<kMode, Form::kPair>(ta, tb, t, q.blocks, 2 * std::min<long long>(tiles, sms / 2), 2, s);
     case Form::kSplit:
-      return launch_tiles<kMode, Form::kSplit>(ta, tb, t, tiles * choice.split, choice.split, s);
+      return launch_tiles<kMode, Form::kSplit>(ta, tb, t, (q.blocks + choice.split - 1) / choice.split, tiles * choice.split,
+                                               choice.split, s);
     default:
-      return launch_tiles<kMode, Form::kSingle>(ta, tb, t, std::min<long long>(tiles, sms), 1, s);
+      return launch_tiles<kMode, Form::kSingle>(ta, tb, t, q.blocks, std::min<long long>(tiles, sms), 1, s);
   }
 }
 

@@ -84,3 +84,37 @@ def test_activations_far_from_zero(act, dt):
         assert act == "relu" or act == "none" or bool(got[0, 14].isnan())
     v = M.moe_linear(torch.nan_to_num(z, nan=0.0), torch.eye(16, device=DEV).to(dt), act=act)[0, :14].cpu()
     assert torch.equal(v, pos * z[0, :14].cpu())
+
+
+LONG = [  # (rows of each group, length of the reduction, width): few rows, few tiles, many tiles, ragged groups
+    ([4], 1 << 20, 16), ([3], (1 << 16) + 24, 9600), ([300], (1 << 19) + 8, 264), ([2048], 1 << 17, 2048),
+    ([200, 0, 130, 7, 500], (1 << 18) + 72, 328), ([16384], 3 * 16384 + 64, 136),
+]
+
+
+@pytest.mark.parametrize("dgrad", [False, True], ids=["forward", "dgrad"])
+@pytest.mark.parametrize("sizes,length,width", LONG)
+def test_long_reductions_are_not_biased(sizes, length, width, dgrad):
+    """bf16 products of one sign over long reductions. Tensor cores truncate when they add, so that the error of one
+    accumulator grows with the length (7e-4 at 2^20); kept to 16384 elements, 1024 steps of 16, it is at most
+    1024 steps of 2^-23, and the partial sums add a rounding each (at most 64 here). A residual takes the bulk of
+    the sum away, so that the rounding of the output does not hide it."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    off = [0]
+    for s in sizes:
+        off.append(off[-1] + s)
+    E, rows = len(sizes), off[-1]
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    a = (torch.rand((rows, length), generator=g, device=DEV) + 0.5).to(BF16)
+    w = (torch.rand((E, length, width) if dgrad else (E, width, length), generator=g, device=DEV) + 0.5).to(BF16)
+    want = torch.zeros((rows, width), dtype=torch.float64, device=DEV)
+    for e, (r0, r1) in R.groups(off):
+        for i in range(0, length, 1 << 14):
+            we = w[e, i:i + (1 << 14)] if dgrad else w[e, :, i:i + (1 << 14)].T
+            want[r0:r1] += a[r0:r1, i:i + (1 << 14)].double() @ we.double()
+    bulk = (-want).to(BF16)
+    y = M.moe_grouped_gemm_dgrad(a, o, w, residual=bulk) if dgrad else M.moe_grouped_gemm(a, o, w, residual=bulk)
+    left = want + bulk.double()
+    tol = (1024 + 64 + 4) * 2.0 ** -23 * want
+    off_by = (y.double() - left).abs() - tol - torch.finfo(BF16).eps / 2 * (left.abs() + tol)
+    assert float(off_by.max()) <= 0, float(((y.double() - left) / want).abs().max())
