@@ -49,11 +49,14 @@
 // 16384 rows, more than in proportion beyond). An accumulator therefore takes
 // chain_blocks() of the reduction only, and the epilogue adds these partial
 // sums, rounded to nearest, in registers, while the MMAs fill the other
-// accumulator. wgrad's fp32 outputs take 768 rows (7e-7; 8192 rows, 4096 x
-// 14336: 702 us; 512 rows an accumulator 718, all rows in one 682), the bf16
-// outputs of the rows modes 16384 elements, a hundredth of half their step, so
-// that no reduction grows less exact than that. In rows mode the adding is an
-// instance of its own (kChained), since its registers spill in the others.
+// accumulator. wgrad's fp32 outputs take 512 rows (relative error of normal
+// sums, root mean square, and the time of 8192 rows, 4096 x 14336 in loops:
+// 256 rows 2.5e-7, 1076 us; 384 3.6e-7, 883; 512 4.8e-7, 801; 768 7.2e-7, 776;
+// a plain fp32 product 9.6e-7 at this length, 2.5e-7 at 1000 rows, 1.5e-6 at
+// 16384), the bf16 outputs of the rows modes 16384 elements, a hundredth of
+// half their step, so that no reduction grows less exact than that. In rows
+// mode the adding is an instance of its own (kChained), since its registers
+// spill in the others.
 #include <cmath>
 
 #include "matmul_common.cuh"
@@ -69,7 +72,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 
 // Blocks of the reduction added in one accumulator (whole stages of the ring).
-constexpr int chain_blocks(MatmulMode m) { return m == MatmulMode::kWgrad ? 12 : 256; }
+constexpr int chain_blocks(MatmulMode m) { return m == MatmulMode::kWgrad ? 8 : 256; }
 constexpr uint32_t kABytes = kBM * kBK * 2;  // one CTA's rows of A
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements
