@@ -498,10 +498,25 @@ def _strided(t, shape, dtype, index, name):
     return t.data_ptr(), ld
 
 
-def _matrix(rows, width, dtype, device):
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: the current one). On another
+    stream than the current one it comes from that stream's memory, where no
+    earlier work of the current stream is still due, and is not handed out
+    again before the current stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
+def _matrix(rows, width, dtype, device, stream):
     """A new matrix whose rows start on 16 bytes (odd widths get padded rows)."""
     wide = (width + 7) // 8 * 8
-    t = torch.empty((rows, wide), dtype=dtype, device=device)
+    t = _empty((rows, wide), dtype, device, stream)
     return t if wide == width else t[:, :width]
 
 
@@ -572,7 +587,7 @@ def _forward(fn, dims, x, offsets, w, bias, act, residual, preact, y, status, st
     pr, ldr = _strided(residual, out, tdt, dev, "residual")
     pz, ldz = _strided(preact, out, tdt, dev, "preact")
     if y is None:
-        y = _matrix(rows, n, tdt, x.device)
+        y = _matrix(rows, n, tdt, x.device, stream)
     py, ldy = _strided(y, out, tdt, dev, "y")
     cfg = MoeGemmConfig(rows, n, k, groups, dt, _act(act), ldx, ldw, ws, ldy, ldr, ldz)
     ps = _plain(status, (1,), torch.int32, dev, "status")
@@ -598,7 +613,7 @@ def _dgrad(fn, dims, dy, offsets, w, z, act, residual, dx, status, stream):
     pz, ldz = _strided(z, out, tdt, dev, "z")
     pr, ldr = _strided(residual, out, tdt, dev, "residual")
     if dx is None:
-        dx = _matrix(rows, k, tdt, dy.device)
+        dx = _matrix(rows, k, tdt, dy.device, stream)
     pdx, ldx = _strided(dx, out, tdt, dev, "dx")
     cfg = MoeGemmConfig(rows, n, k, groups, dt, _act(act), ldx, ldw, ws, ldy, ldr, ldz)
     ps = _plain(status, (1,), torch.int32, dev, "status")
@@ -619,7 +634,7 @@ def _wgrad(fn, dims, dy, offsets, x, groups, dw, dbias, status, stream):
     px, ldx = _strided(x, (rows, k), dy.dtype, dev, "x")
     shape = (n, k) if dims == 2 else (groups, n, k)
     if dw is None:
-        dw = torch.empty(shape, dtype=torch.float32, device=dy.device)
+        dw = _empty(shape, torch.float32, dy.device, stream)
     pdw = _plain(dw, shape, torch.float32, dev, "dw")
     pdb = _plain(dbias, shape[:-1], torch.float32, dev, "dbias")
     cfg = MoeGemmConfig(rows, n, k, groups, dt, MOE_ACT_NONE, ldx, 0, 0, ldy, 0, 0)
@@ -640,7 +655,10 @@ def moe_grouped_gemm(x, offsets, w, bias=None, act="none", residual=None, preact
     fp32; act "none", "relu", "gelu", "gelu_tanh" or "silu"; preact [rows, n]
     receives the argument of act. Rows of matrices may lie apart (bf16 row
     strides: multiples of 8). Rows outside every group are left as they were
-    (uninitialised in a y made here). Returns y."""
+    (uninitialised in a y made here). residual may be y; no other argument may
+    share memory with an output. stream: where the call runs (default: the
+    device's current one), after whatever made its arguments; other streams
+    wait for it before they read its outputs. Returns y."""
     return _forward("moe_grouped_gemm", 3, x, _given(offsets), w, bias, act, residual, preact, y, status, stream)
 
 
@@ -688,7 +706,7 @@ def moe_act_backward(dy, z, act, dz=None, stream=None):
     pdy, ldy = _strided(dy, shape, dy.dtype, dev, "dy")
     pz, ldz = _strided(z, shape, dy.dtype, dev, "z")
     if dz is None:
-        dz = _matrix(*shape, dy.dtype, dy.device)
+        dz = _matrix(*shape, dy.dtype, dy.device, stream)
     pdz, ldr = _strided(dz, shape, dy.dtype, dev, "dz")
     cfg = MoeGemmConfig(shape[0], shape[1], 1, 1, dt, _act(act), 0, 0, 0, ldy, ldr, ldz)
     _enqueue("moe_act_backward", dev, stream, cfg, pdy, pz, pdz)
@@ -706,7 +724,7 @@ def moe_dropout(x, p, rng=None, offset=0, residual=None, y=None, stream=None):
     px, ldx = _strided(x, shape, x.dtype, dev, "x")
     pr, ldr = _strided(residual, shape, x.dtype, dev, "residual")
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        y = _empty(shape, x.dtype, x.device, stream)
     py, ldy = _strided(y, shape, x.dtype, dev, "y")
     _enqueue("moe_dropout", dev, stream, shape[0], shape[1], dt, px, ldx, pr, ldr, py, ldy, p,
              _plain(rng, (2,), torch.int64, dev, "rng"), offset)
@@ -728,7 +746,7 @@ def moe_unpermute_combine_dropout(cfg, y_perm, dest_row, topk_gate, p, rng=None,
     pg = _plain(topk_gate, (cfg.T, cfg.k), torch.float32, dev, "topk_gate")
     pr = _plain(residual, (cfg.T, cfg.d), dt, dev, "residual")
     if y is None:
-        y = torch.empty((cfg.T, cfg.d), dtype=dt, device=y_perm.device)
+        y = _empty((cfg.T, cfg.d), dt, y_perm.device, stream)
     py = _plain(y, (cfg.T, cfg.d), dt, dev, "y")
     _enqueue("moe_unpermute_combine_dropout", dev, stream, cfg, pp, pd, pg, pr, p,
              _plain(rng, (2,), torch.int64, dev, "rng"), offset, py)

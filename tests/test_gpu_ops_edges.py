@@ -128,3 +128,58 @@ def test_weight_gradient_is_as_exact_as_promised(rows, n, k):
     x = torch.randn((rows, k), generator=g, device=DEV).to(BF16)
     want = dy.double().T @ x.double()
     assert float((M.moe_linear_wgrad(dy, x).double() - want).norm() / want.norm()) <= 6e-7
+
+
+def calls_on_a_stream():
+    g = torch.Generator().manual_seed(5)
+    rnd = lambda *shape: torch.randn(shape, generator=g).to(BF16).to(DEV)
+    x, w, dy, z = rnd(1000, 256), rnd(2, 256, 256), rnd(1000, 256), rnd(1000, 256)
+    o, rng = torch.tensor([0, 400, 1000], dtype=torch.int32, device=DEV), torch.tensor([1, 2], device=DEV)
+    cfg = M.config(500, 256, 4, 2, 128, "bf16", "identity")
+    dest = torch.randperm(1000, generator=g).reshape(500, 2).to(torch.int32).to(DEV)
+    gate = torch.rand((500, 2), generator=g).to(DEV)
+    return {
+        "grouped": lambda s: M.moe_grouped_gemm(x, o, w, stream=s),
+        "grouped_dgrad": lambda s: M.moe_grouped_gemm_dgrad(dy, o, w, stream=s),
+        "grouped_wgrad": lambda s: M.moe_grouped_gemm_wgrad(dy, o, x, stream=s),
+        "linear": lambda s: M.moe_linear(x, w[0], stream=s),
+        "linear_dgrad": lambda s: M.moe_linear_dgrad(dy, w[0], stream=s),
+        "linear_wgrad": lambda s: M.moe_linear_wgrad(dy, x, stream=s),
+        "act_backward": lambda s: M.moe_act_backward(dy, z, "silu", stream=s),
+        "dropout": lambda s: M.moe_dropout(x, 0.5, rng, stream=s),
+        "combine_dropout": lambda s: M.moe_unpermute_combine_dropout(cfg, x, dest, gate, 0.5, rng, stream=s),
+    }
+
+
+def written_on_another_stream(call):
+    """The call's output, made by the call on another stream, while the current stream still has to write memory that
+    was freed just before, and read again on the current stream after a wait, while the other stream goes on."""
+    ref = call(None).clone()
+    side = torch.cuda.Stream()
+    call(side)  # any first-call set-up
+    torch.cuda.synchronize()
+    freed = torch.empty_like(ref)
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    freed.fill_(7)
+    del freed
+    y = call(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref)
+    side.wait_stream(torch.cuda.current_stream())
+    y = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(100_000_000)
+    copy = y.clone()
+    del y
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            torch.empty_like(ref).fill_(9)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, ref)
+
+
+@pytest.mark.parametrize("name", ["grouped", "grouped_dgrad", "grouped_wgrad", "linear", "linear_dgrad", "linear_wgrad",
+                                  "act_backward", "dropout", "combine_dropout"])
+def test_outputs_made_for_another_stream(name):
+    written_on_another_stream(calls_on_a_stream()[name])
