@@ -207,9 +207,25 @@ def moe_gemm_tiles_used(cfg: MoeConfig) -> int:
     return tiles.value
 
 
-def workspace(cfg: MoeConfig, op: int, device) -> torch.Tensor:
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: the current one). On another
+    stream than the current one it comes from that stream's memory, where no
+    earlier work of the current stream is still due, and is not handed out
+    again before the current stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
+def workspace(cfg: MoeConfig, op: int, device, stream=None) -> torch.Tensor:
+    """Memory for one `op` at a time; stream: another stream than the current one that the op will run on."""
     n = moe_workspace_size(cfg, op)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    return _empty((max(n, 256),), torch.uint8, device, stream)
 
 
 def moe_pack_weights(cfg, w_gate, w_up, w13_packed=None, stream=None):
@@ -217,7 +233,7 @@ def moe_pack_weights(cfg, w_gate, w_up, w13_packed=None, stream=None):
     _check(w_gate, (cfg.E, cfg.d_ff, cfg.d), dt, "w_gate")
     _check(w_up, (cfg.E, cfg.d_ff, cfg.d), dt, "w_up")
     if w13_packed is None:
-        w13_packed = torch.empty((cfg.E, 2 * cfg.d_ff, cfg.d), dtype=dt, device=_dev(w_gate))
+        w13_packed = _empty((cfg.E, 2 * cfg.d_ff, cfg.d), dt, _dev(w_gate), stream)
     _check(w13_packed, (cfg.E, 2 * cfg.d_ff, cfg.d), dt, "w13_packed")
     _rc("moe_pack_weights", lib().moe_pack_weights(ctypes.byref(cfg), _ptr(w_gate), _ptr(w_up), _ptr(w13_packed),
                                                    _stream(stream)))
@@ -233,9 +249,9 @@ def moe_route(cfg, h, w_router, bias=None, logits_out=None, topk_idx=None, topk_
     _check(bias, (cfg.E,), torch.float32, "bias")
     _check(logits_out, (cfg.T, cfg.E), torch.float32, "logits_out")
     if topk_idx is None:
-        topk_idx = torch.empty((cfg.T, cfg.k), dtype=torch.int32, device=dev)
+        topk_idx = _empty((cfg.T, cfg.k), torch.int32, dev, stream)
     if topk_gate is None:
-        topk_gate = torch.empty((cfg.T, cfg.k), dtype=torch.float32, device=dev)
+        topk_gate = _empty((cfg.T, cfg.k), torch.float32, dev, stream)
     _check(topk_idx, (cfg.T, cfg.k), torch.int32, "topk_idx")
     _check(topk_gate, (cfg.T, cfg.k), torch.float32, "topk_gate")
     _rc("moe_route", lib().moe_route(ctypes.byref(cfg), _ptr(h), _ptr(w_router), _ptr(bias), _ptr(logits_out),
@@ -251,14 +267,14 @@ def moe_permute(cfg, h, topk_idx, out=None, ws=None, status=None, stream=None):
     _check(h, (cfg.T, cfg.d), dt, "h")
     _check(topk_idx, (cfg.T, cfg.k), torch.int32, "topk_idx")
     if out is None:
-        out = dict(routed_counts=torch.empty(cfg.E, dtype=torch.int32, device=dev),
-                   counts=torch.empty(cfg.E, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(cfg.E + 1, dtype=torch.int32, device=dev),
-                   dest_row=torch.empty((cfg.T, cfg.k), dtype=torch.int32, device=dev),
-                   perm_src=torch.empty(max(A, 1), dtype=torch.int32, device=dev),
-                   x_perm=torch.empty((max(A, 1), cfg.d), dtype=dt, device=dev))
+        out = dict(routed_counts=_empty(cfg.E, torch.int32, dev, stream),
+                   counts=_empty(cfg.E, torch.int32, dev, stream),
+                   offsets=_empty(cfg.E + 1, torch.int32, dev, stream),
+                   dest_row=_empty((cfg.T, cfg.k), torch.int32, dev, stream),
+                   perm_src=_empty(max(A, 1), torch.int32, dev, stream),
+                   x_perm=_empty((max(A, 1), cfg.d), dt, dev, stream))
     if ws is None:
-        ws = workspace(cfg, MOE_OP_PERMUTE, dev)
+        ws = workspace(cfg, MOE_OP_PERMUTE, dev, stream)
     _rc("moe_permute", lib().moe_permute(
         ctypes.byref(cfg), _ptr(h), _ptr(topk_idx), _ptr(out["routed_counts"]), _ptr(out["counts"]),
         _ptr(out["offsets"]), _ptr(out["dest_row"]), _ptr(out["perm_src"]), _ptr(out["x_perm"]), _ptr(ws),
@@ -277,9 +293,9 @@ def moe_grouped_ffn(cfg, x_perm, offsets, w13_packed=None, w_down=None, y_perm=N
     if cfg.expert_kind == MOE_EXPERT_SWIGLU:
         _check_expert_weights(cfg, w13_packed, w_down)
     if y_perm is None:
-        y_perm = torch.empty((rows, cfg.d), dtype=dt, device=dev)
+        y_perm = _empty((rows, cfg.d), dt, dev, stream)
     if ws is None:
-        ws = workspace(cfg, MOE_OP_GROUPED_FFN, dev)
+        ws = workspace(cfg, MOE_OP_GROUPED_FFN, dev, stream)
     _rc("moe_grouped_ffn", lib().moe_grouped_ffn(
         ctypes.byref(cfg), _ptr(x_perm), _ptr(offsets), _ptr(w13_packed), _ptr(w_down), _ptr(y_perm), _ptr(ws),
         ws.numel(), _ptr(status), _stream(stream)))
@@ -291,7 +307,7 @@ def moe_unpermute_combine(cfg, y_perm, dest_row, topk_gate, y=None, status=None,
     _check(dest_row, (cfg.T, cfg.k), torch.int32, "dest_row")
     _check(topk_gate, (cfg.T, cfg.k), torch.float32, "topk_gate")
     if y is None:
-        y = torch.empty((cfg.T, cfg.d), dtype=dt, device=_dev(y_perm))
+        y = _empty((cfg.T, cfg.d), dt, _dev(y_perm), stream)
     _check(y, (cfg.T, cfg.d), dt, "y")
     _rc("moe_unpermute_combine", lib().moe_unpermute_combine(
         ctypes.byref(cfg), _ptr(y_perm), _ptr(dest_row), _ptr(topk_gate), _ptr(y), _ptr(status), _stream(stream)))
@@ -316,10 +332,10 @@ def moe_layer_forward(cfg, h, w_router, bias=None, w13_packed=None, w_down=None,
     _check(routed_counts, (cfg.E,), torch.int32, "routed_counts")
     _check(counts, (cfg.E,), torch.int32, "counts")
     if y is None:
-        y = torch.empty((cfg.T, cfg.d), dtype=dt, device=dev)
+        y = _empty((cfg.T, cfg.d), dt, dev, stream)
     _check(y, (cfg.T, cfg.d), dt, "y")
     if ws is None:
-        ws = workspace(cfg, MOE_OP_LAYER, dev)
+        ws = workspace(cfg, MOE_OP_LAYER, dev, stream)
     args = (ctypes.byref(cfg), _ptr(h), _ptr(w_router), _ptr(bias), _ptr(w13_packed), _ptr(w_down), _ptr(y),
             _ptr(topk_idx), _ptr(topk_gate), _ptr(routed_counts), _ptr(counts), _ptr(ws), ws.numel(), _ptr(status),
             _stream(stream))
@@ -352,12 +368,12 @@ def moe_permute_static_scratch(cfg, h, topk_idx, out=None, status=None, stream=N
     _check(h, (cfg.T, cfg.d), dt, "h")
     _check(topk_idx, (cfg.T, cfg.k), torch.int32, "topk_idx")
     if out is None:
-        out = dict(routed_counts=torch.empty(cfg.E, dtype=torch.int32, device=dev),
-                   counts=torch.empty(cfg.E, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(cfg.E + 1, dtype=torch.int32, device=dev),
-                   dest_row=torch.empty((cfg.T, cfg.k), dtype=torch.int32, device=dev),
-                   perm_src=torch.empty(max(A, 1), dtype=torch.int32, device=dev),
-                   x_perm=torch.empty((max(A, 1), cfg.d), dtype=dt, device=dev))
+        out = dict(routed_counts=_empty(cfg.E, torch.int32, dev, stream),
+                   counts=_empty(cfg.E, torch.int32, dev, stream),
+                   offsets=_empty(cfg.E + 1, torch.int32, dev, stream),
+                   dest_row=_empty((cfg.T, cfg.k), torch.int32, dev, stream),
+                   perm_src=_empty(max(A, 1), torch.int32, dev, stream),
+                   x_perm=_empty((max(A, 1), cfg.d), dt, dev, stream))
     _rc("moe_permute_static_scratch", lib().moe_permute_static_scratch(
         ctypes.byref(cfg), _ptr(h), _ptr(topk_idx), _ptr(out["routed_counts"]), _ptr(out["counts"]),
         _ptr(out["offsets"]), _ptr(out["dest_row"]), _ptr(out["perm_src"]), _ptr(out["x_perm"]), _ptr(status),
@@ -372,8 +388,8 @@ def moe_pack_weights_backward(cfg, w13_packed, w_down, stream=None):
     dev = _dev(w13_packed)
     _check(w13_packed, (cfg.E, 2 * cfg.d_ff, cfg.d), dt, "w13_packed")
     _check(w_down, (cfg.E, cfg.d, cfg.d_ff), dt, "w_down")
-    w13_t = torch.empty((cfg.E, cfg.d, 2 * cfg.d_ff), dtype=dt, device=dev)
-    w_down_t = torch.empty((cfg.E, cfg.d_ff, cfg.d), dtype=dt, device=dev)
+    w13_t = _empty((cfg.E, cfg.d, 2 * cfg.d_ff), dt, dev, stream)
+    w_down_t = _empty((cfg.E, cfg.d_ff, cfg.d), dt, dev, stream)
     _rc("moe_pack_weights_backward", lib().moe_pack_weights_backward(
         ctypes.byref(cfg), _ptr(w13_packed), _ptr(w_down), _ptr(w13_t), _ptr(w_down_t), _stream(stream)))
     return w13_t, w_down_t
@@ -392,13 +408,13 @@ def moe_layer_backward(cfg, h, w_router, w13_packed, w13_t, w_down_t, dy, fwd_ws
     _check(w13_t, (cfg.E, cfg.d, 2 * cfg.d_ff), dt, "w13_t")
     _check(w_down_t, (cfg.E, cfg.d_ff, cfg.d), dt, "w_down_t")
     _check(dy, (cfg.T, cfg.d), dt, "dy")
-    out = dict(dh=torch.empty((cfg.T, cfg.d), dtype=dt, device=dev),
-               dw_router=torch.empty((cfg.E, cfg.d), dtype=torch.float32, device=dev),
-               dbias=torch.empty(cfg.E, dtype=torch.float32, device=dev) if with_bias else None,
-               dw13=torch.empty((cfg.E, 2 * cfg.d_ff, cfg.d), dtype=torch.float32, device=dev),
-               dw_down=torch.empty((cfg.E, cfg.d, cfg.d_ff), dtype=torch.float32, device=dev))
+    out = dict(dh=_empty((cfg.T, cfg.d), dt, dev, stream),
+               dw_router=_empty((cfg.E, cfg.d), torch.float32, dev, stream),
+               dbias=_empty(cfg.E, torch.float32, dev, stream) if with_bias else None,
+               dw13=_empty((cfg.E, 2 * cfg.d_ff, cfg.d), torch.float32, dev, stream),
+               dw_down=_empty((cfg.E, cfg.d, cfg.d_ff), torch.float32, dev, stream))
     if ws is None:
-        ws = workspace(cfg, MOE_OP_BACKWARD, dev)
+        ws = workspace(cfg, MOE_OP_BACKWARD, dev, stream)
     _rc("moe_layer_backward", lib().moe_layer_backward(
         ctypes.byref(cfg), _ptr(h), _ptr(w_router), _ptr(w13_packed), _ptr(w13_t), _ptr(w_down_t), _ptr(dy),
         _ptr(out["dh"]), _ptr(out["dw_router"]), _ptr(out["dbias"]), _ptr(out["dw13"]), _ptr(out["dw_down"]),
@@ -426,9 +442,11 @@ def moe_mxfp8_quantize(x, q=None, sf=None, counts=None, status=None, stream=None
     rows, cols = x.shape
     dev = _dev(x)
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        q = _empty((rows, cols), torch.uint8, dev, stream)
     if sf is None:
-        sf = torch.zeros(max(mxfp8_scale_bytes(rows, cols), 1), dtype=torch.uint8, device=dev)
+        sf = _empty(max(mxfp8_scale_bytes(rows, cols), 1), torch.uint8, dev, stream)
+        with torch.cuda.stream(stream):
+            sf.zero_()
     _check(q, (rows, cols), torch.uint8, "q")
     if sf.numel() < mxfp8_scale_bytes(rows, cols) or sf.dtype != torch.uint8:
         raise ValueError("sf too small")
@@ -445,8 +463,8 @@ def moe_pack_weights_mxfp8(cfg, w13_packed, w_down, counts=None, stream=None):
     _check(w13_packed, (cfg.E, 2 * cfg.d_ff, cfg.d), torch.bfloat16, "w13_packed")
     _check(w_down, (cfg.E, cfg.d, cfg.d_ff), torch.bfloat16, "w_down")
     dev = _dev(w13_packed)
-    a = torch.empty(moe_mxfp8_weights_size(cfg, 0), dtype=torch.uint8, device=dev)
-    b = torch.empty(moe_mxfp8_weights_size(cfg, 1), dtype=torch.uint8, device=dev)
+    a = _empty(moe_mxfp8_weights_size(cfg, 0), torch.uint8, dev, stream)
+    b = _empty(moe_mxfp8_weights_size(cfg, 1), torch.uint8, dev, stream)
     _rc("moe_pack_weights_mxfp8", lib().moe_pack_weights_mxfp8(ctypes.byref(cfg), _ptr(w13_packed), _ptr(w_down),
                                                                _ptr(a), _ptr(b), _ptr(counts), _stream(stream)))
     return a, b
@@ -496,21 +514,6 @@ def _strided(t, shape, dtype, index, name):
     if (st[-1] != 1 and width > 1) or ld < width:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {st})")
     return t.data_ptr(), ld
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on `stream` (None: the current one). On another
-    stream than the current one it comes from that stream's memory, where no
-    earlier work of the current stream is still due, and is not handed out
-    again before the current stream is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    current = torch.cuda.current_stream(device)
-    if current != stream:
-        t.record_stream(current)
-    return t
 
 
 def _matrix(rows, width, dtype, device, stream):

@@ -183,3 +183,36 @@ def written_on_another_stream(call):
                                   "act_backward", "dropout", "combine_dropout"])
 def test_outputs_made_for_another_stream(name):
     written_on_another_stream(calls_on_a_stream()[name])
+
+
+def layer_calls_on_a_stream():
+    g = torch.Generator().manual_seed(6)
+    rnd = lambda *shape: (torch.randn(shape, generator=g) / 8).to(BF16).to(DEV)
+    T, d, E, k, F = 512, 256, 8, 2, 256
+    cfg = M.config(T, d, E, k, F)
+    h, wr, wg, wu, wd = rnd(T, d), rnd(E, d), rnd(E, F, d), rnd(E, F, d), rnd(E, d, F)
+    w13 = M.moe_pack_weights(cfg, wg, wu)
+    idx, gate = M.moe_route(cfg, h, wr)
+    pm = M.moe_permute(cfg, h, idx)
+    yp = M.moe_grouped_ffn(cfg, pm["x_perm"], pm["offsets"], w13, wd)
+    fwd_ws = M.workspace(cfg, M.MOE_OP_LAYER, DEV)
+    M.moe_layer_forward(cfg, h, wr, w13_packed=w13, w_down=wd, ws=fwd_ws)
+    w13_t, wd_t = M.moe_pack_weights_backward(cfg, w13, wd)
+    return {
+        "pack": lambda s: M.moe_pack_weights(cfg, wg, wu, stream=s),
+        "route": lambda s: M.moe_route(cfg, h, wr, stream=s)[1],
+        "permute": lambda s: M.moe_permute(cfg, h, idx, stream=s)["x_perm"],
+        "ffn": lambda s: M.moe_grouped_ffn(cfg, pm["x_perm"], pm["offsets"], w13, wd, stream=s),
+        "combine": lambda s: M.moe_unpermute_combine(cfg, yp, pm["dest_row"], gate, stream=s),
+        "layer": lambda s: M.moe_layer_forward(cfg, h, wr, w13_packed=w13, w_down=wd, stream=s),
+        "pack_backward": lambda s: M.moe_pack_weights_backward(cfg, w13, wd, stream=s)[0],
+        "backward": lambda s: M.moe_layer_backward(cfg, h, wr, w13, w13_t, wd_t, h, fwd_ws, stream=s)["dw13"],
+        "quantize": lambda s: M.moe_mxfp8_quantize(h, stream=s)[1],
+        "pack_mxfp8": lambda s: M.moe_pack_weights_mxfp8(cfg, w13, wd, stream=s)[0],
+    }
+
+
+@pytest.mark.parametrize("name", ["pack", "route", "permute", "ffn", "combine", "layer", "pack_backward", "backward",
+                                  "quantize", "pack_mxfp8"])
+def test_outputs_of_the_layer_made_for_another_stream(name):
+    written_on_another_stream(layer_calls_on_a_stream()[name])

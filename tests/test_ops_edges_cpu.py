@@ -1,0 +1,66 @@
+"""The operators around the layer on the CPU: limits at their edges, what the
+binding makes for a call, and which kernel form a call takes."""
+import ast
+import inspect
+
+import pytest
+import torch
+
+import combine_router_gemm_softmax_b200 as M
+from combine_router_gemm_softmax_b200 import _lib
+
+
+@pytest.fixture(scope="module")
+def L():
+    from combine_router_gemm_softmax_b200 import build
+    build.build()
+    return M.lib()
+
+
+def test_calls_with_a_stream_make_their_tensors_for_it():
+    """Every function that takes a stream makes outputs and workspaces by _empty (or workspace), and hands it the
+    stream: memory of the current stream may still be written by earlier work there."""
+    tree = ast.parse(inspect.getsource(_lib))
+    made = 0
+    for f in tree.body:
+        if not isinstance(f, ast.FunctionDef) or f.name == "_empty" or "stream" not in [a.arg for a in f.args.args]:
+            continue
+        for call in ast.walk(f):
+            if not isinstance(call, ast.Call):
+                continue
+            name = ast.unparse(call.func)
+            assert name not in ("torch.empty", "torch.zeros", "torch.full", "torch.empty_like"), f.name
+            if name in ("_empty", "_matrix", "workspace"):
+                made += 1
+                assert ast.unparse(call.args[-1]) == "stream", f.name
+    assert made > 30
+
+
+class Other:
+    """A stream that is not the current one, and the tensors' record of it."""
+
+    def __init__(self, log):
+        self.log = log
+
+    def __enter__(self):
+        self.log.append("enter")
+
+    def __exit__(self, *exc):
+        self.log.append("exit")
+
+
+def test_memory_for_another_stream(monkeypatch):
+    log = []
+    empty = torch.empty
+
+    class Recorded:
+        def record_stream(self, s):
+            log.append(("record", s))
+
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: log.append("empty") or Recorded())
+    _lib._empty((2, 3), torch.float32, "cpu", Other(log))
+    assert log == ["enter", "empty", "exit", ("record", "current")]
+    monkeypatch.setattr(torch, "empty", empty)
+    assert _lib._empty((2, 3), torch.float32, "cpu", None).shape == (2, 3)
