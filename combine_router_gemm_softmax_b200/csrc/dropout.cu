@@ -159,7 +159,7 @@ template <typename T, bool kDrop, bool kResidual>
 cudaError_t launch_typed(Matrices m, const DropoutArgs& d, cudaStream_t s) {
   constexpr int N = Row16<T>::N;
   const bool vec = m.cols % N == 0 && m.ldx % N == 0 && m.ldy % N == 0 && (!kResidual || m.ldr % N == 0);
-  m.vpr = vec ? m.cols / N : (m.cols + 3) / 4;
+  m.vpr = vec ? m.cols / N : static_cast<int>((m.cols + 3LL) / 4);  // up to 2^31 - 1 columns
   // Threads for a whole number of rows: every thread keeps its column. Enough
   // for a row at least, and no more than fill the SMs.
   const long long units = static_cast<long long>(m.rows) * m.vpr;

@@ -216,3 +216,19 @@ def layer_calls_on_a_stream():
                                   "quantize", "pack_mxfp8"])
 def test_outputs_of_the_layer_made_for_another_stream(name):
     written_on_another_stream(layer_calls_on_a_stream()[name])
+
+
+@pytest.mark.parametrize("cols", [(1 << 31) - 1, (1 << 31) - 3, (1 << 31) - 8])
+def test_dropout_of_the_widest_rows(cols):
+    """One row of up to 2^31 - 1 columns: its ends, and a piece in the middle, against the generator's words."""
+    import numpy as np
+    p, seed, at = 0.5, 5, 7
+    x = torch.ones((1, cols), dtype=BF16, device=DEV)
+    y = M.moe_dropout(x, p, torch.tensor([seed, at], device=DEV))
+    for first in (0, (1 << 30) - 32, cols // 4 * 4 - 64):
+        last = min(first + 68, cols)
+        quads = np.arange(first // 4, (last + 3) // 4, dtype=np.uint64)
+        words = np.stack(R.philox4x32([quads, np.zeros_like(quads), np.full_like(quads, at), np.zeros_like(quads)],
+                                      (seed, 0)), axis=1).reshape(-1)[:last - first]
+        want = torch.from_numpy((words >= 1 << 31).astype(np.float64)) * 2
+        assert torch.equal(y[0, first:last].cpu().double(), want), first
