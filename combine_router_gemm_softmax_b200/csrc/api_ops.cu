@@ -72,12 +72,20 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   return p;
 }
 
-cudaError_t launch_product(int dtype, MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_F32)
-    return mode == MatmulMode::kForward && matmul_few_rows_f32(a) ? launch_matmul_rows_f32(a, s)
-                                                                  : launch_matmul_f32(mode, a, s);
-  if (mode == MatmulMode::kForward && matmul_few_rows(a)) return launch_matmul_rows(a, s);
-  return launch_matmul_tc(mode, a, s);
+MatmulPlan plan_product(int dtype, MatmulMode mode, const MatmulArgs& a, int sms) {
+  const bool f32 = dtype == MOE_DTYPE_F32;
+  if (mode == MatmulMode::kForward && (f32 ? matmul_few_rows_f32(a) : matmul_few_rows(a, sms)))
+    return {Form::kFewRows, 0, 1, 0};
+  return f32 ? plan_matmul_f32(mode, a, sms) : plan_matmul_tc(mode, a, sms);
+}
+
+int launch_product(int dtype, MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+  const bool f32 = dtype == MOE_DTYPE_F32;
+  const int sms = device_sm_count();
+  const MatmulPlan plan = plan_product(dtype, mode, a, sms);
+  if (plan.tiles >= 1LL << 31 && !f32) return MOE_ERR_UNSUPPORTED;  // the tiles' 32-bit indices
+  if (plan.form == Form::kFewRows) return rc_of(f32 ? launch_matmul_rows_f32(a, s) : launch_matmul_rows(a, sms, s));
+  return rc_of(f32 ? launch_matmul_f32(mode, plan, a, sms, s) : launch_matmul_tc(mode, plan, a, sms, s));
 }
 
 int forward(const moe_gemm_config* cfg, bool dense, const void* x, const int32_t* offsets, const void* w,
@@ -98,7 +106,7 @@ int forward(const moe_gemm_config* cfg, bool dense, const void* x, const int32_t
   a.d = y, a.act = c.act, a.status = status;
   a.vec = c.k % 4 == 0 && c.ldx % 4 == 0 && c.ldw % 4 == 0 && c.w_stride % 4 == 0;
   a.vec_out = c.ldy % 4 == 0 && (!residual || c.ldr % 4 == 0) && (!preact || c.ldz % 4 == 0);
-  return rc_of(launch_product(c.dtype, MatmulMode::kForward, a, s));
+  return launch_product(c.dtype, MatmulMode::kForward, a, s);
 }
 
 int dgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t* offsets, const void* w, const void* z,
@@ -118,7 +126,7 @@ int dgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
   a.d = dx, a.act = c.act, a.status = status;
   a.vec = c.n % 4 == 0 && c.k % 4 == 0 && c.ldy % 4 == 0 && c.ldw % 4 == 0 && c.w_stride % 4 == 0;
   a.vec_out = c.ldx % 4 == 0 && (!residual || c.ldr % 4 == 0) && (!z || c.ldz % 4 == 0);
-  return rc_of(launch_product(c.dtype, MatmulMode::kDgrad, a, s));
+  return launch_product(c.dtype, MatmulMode::kDgrad, a, s);
 }
 
 int wgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t* offsets, const void* x, float* dw,
@@ -144,7 +152,7 @@ int wgrad(const moe_gemm_config* cfg, bool dense, const void* dy, const int32_t*
     a.d = dw, a.status = status;
     a.vec = c.n % 4 == 0 && c.k % 4 == 0 && c.ldy % 4 == 0 && c.ldx % 4 == 0;
     a.vec_out = c.k % 4 == 0 && aligned(dw, 16);
-    const int rc = rc_of(launch_product(c.dtype, MatmulMode::kWgrad, a, s));
+    const int rc = launch_product(c.dtype, MatmulMode::kWgrad, a, s);
     if (rc != MOE_OK) return rc;
   }
   if (dbias)

@@ -221,18 +221,18 @@ static long long row_blocks(const MatmulArgs& a) { return (a.rows + 7LL) / 8 + s
 //    11.2 / 13.7, k 2048, n 16, 2048 rows 3.8 / 9.9 (k 128, n 640, 256 rows, more
 //    than one wave: 6.3 / 3.6); on all of them if the reads stay small: k 1408,
 //    n 2048, 64 rows, 46 MB 8.0 / 8.8 (k = n = 4096, 24 rows, 100 MB 15.5 / 13.9).
-bool matmul_few_rows(const MatmulArgs& a) {
+bool matmul_few_rows(const MatmulArgs& a, int sms) {
   if (a.rows <= 8 || 2LL * a.rows <= a.groups) return true;
-  const long long blocks = row_blocks(a), warps = (a.n + 31) / 32 * 4 * blocks, sms = device_sm_count();
-  return warps <= 7 * sms || (warps <= 16 * sms && blocks * a.n * a.k <= (24LL << 20));
+  const long long blocks = row_blocks(a), warps = (a.n + 31) / 32 * 4 * blocks;
+  return warps <= 7LL * sms || (warps <= 16LL * sms && blocks * a.n * a.k <= (24LL << 20));
 }
 
-cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s) {
+cudaError_t launch_matmul_rows(const MatmulArgs& a, int sms, cudaStream_t s) {
   const long long blocks = row_blocks(a);
   // The cut with the most warps that still fit on the SMs at once (16 each):
   // with k 4096, n 4096 and one row 16 features x 8 warps take 8.2 us, 32 x 8
   // 10.1 and 32 x 4 15.5; with n 14336, 26.7, 25.4 and 23.8 us.
-  const long long fit = 16LL * device_sm_count();
+  const long long fit = 16LL * sms;
   if ((a.n + 15) / 16 * blocks * 8 <= fit) return launch_features<1, 8>(a, blocks, s);
   if ((a.n + 31) / 32 * blocks * 8 <= fit) return launch_features<2, 8>(a, blocks, s);
   return launch_features<2, 4>(a, blocks, s);

@@ -283,42 +283,47 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 3) matmul_simt_kerne
 }
 
 template <MatmulMode kMode, bool kVec>
-cudaError_t launch_tiles(const MatmulArgs& a, cudaStream_t s) {
-  const int sms = device_sm_count();
-  // no more than these row tiles exist, however the rows fall to the groups
-  auto tiles = [&](long long bt) {
-    const long long tn = (a.n + bt - 1) / bt;
-    const long long tm = kMode == MatmulMode::kWgrad ? static_cast<long long>(a.groups) * ((a.m + bt - 1) / bt)
-                                                     : a.rows / bt + a.groups;
-    return tm * tn;
-  };
-  if (tiles(128) >= sms)
-    return launch_kernel(matmul_simt_kernel<kMode, kVec, 128>, dim3(static_cast<unsigned>(std::min<long long>(tiles(128), 2 * sms))),
-                         dim3(kThreads), 0, s, true, 1, a);
-  const long long t = tiles(64);
-  const int depth = kMode == MatmulMode::kWgrad ? a.rows : a.k;
-  int split = 1;
-  while (split < 8 && t * split * 2 <= 3 * sms && depth / (split * 2) >= 64) split *= 2;
-  const long long grid = std::min<long long>(t, 3 * sms) * split;
+cudaError_t launch_tiles(const MatmulPlan& plan, const MatmulArgs& a, int sms, cudaStream_t s) {
+  if (plan.bn == 128)
+    return launch_kernel(matmul_simt_kernel<kMode, kVec, 128>,
+                         dim3(static_cast<unsigned>(std::min<long long>(plan.tiles, 2 * sms))), dim3(kThreads), 0, s, true,
+                         1, a);
+  const long long grid = std::min<long long>(plan.tiles, 3 * sms) * plan.split;
   return launch_kernel(matmul_simt_kernel<kMode, kVec, 64>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, true,
-                       static_cast<unsigned>(split), a);
+                       static_cast<unsigned>(plan.split), a);
 }
 
 template <MatmulMode kMode>
-cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
-  return a.vec ? launch_tiles<kMode, true>(a, s) : launch_tiles<kMode, false>(a, s);
+cudaError_t launch_mode(const MatmulPlan& plan, const MatmulArgs& a, int sms, cudaStream_t s) {
+  return a.vec ? launch_tiles<kMode, true>(plan, a, sms, s) : launch_tiles<kMode, false>(plan, a, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+MatmulPlan plan_matmul_f32(MatmulMode mode, const MatmulArgs& a, int sms) {
+  // no more than these row tiles exist, however the rows fall to the groups
+  auto tiles = [&](long long bt) {
+    const long long tn = (a.n + bt - 1) / bt;
+    const long long tm = mode == MatmulMode::kWgrad ? static_cast<long long>(a.groups) * ((a.m + bt - 1) / bt)
+                                                    : a.rows / bt + a.groups;
+    return tm * tn;
+  };
+  if (tiles(128) >= sms) return {Form::kSingle, 128, 1, tiles(128)};
+  const long long t = tiles(64);
+  const int depth = mode == MatmulMode::kWgrad ? a.rows : a.k;
+  int split = 1;
+  while (split < 8 && t * split * 2 <= 3 * sms && depth / (split * 2) >= 64) split *= 2;
+  return {split > 1 ? Form::kSplit : Form::kSingle, 64, split, t};
+}
+
+cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulPlan& plan, const MatmulArgs& a, int sms, cudaStream_t s) {
   switch (mode) {
     case MatmulMode::kForward:
-      return launch_mode<MatmulMode::kForward>(a, s);
+      return launch_mode<MatmulMode::kForward>(plan, a, sms, s);
     case MatmulMode::kDgrad:
-      return launch_mode<MatmulMode::kDgrad>(a, s);
+      return launch_mode<MatmulMode::kDgrad>(plan, a, sms, s);
     default:
-      return launch_mode<MatmulMode::kWgrad>(a, s);
+      return launch_mode<MatmulMode::kWgrad>(plan, a, sms, s);
   }
 }
 

@@ -77,8 +77,6 @@ constexpr uint32_t kABytes = kBM * kBK * 2;  // one CTA's rows of A
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 64 * 128;  // an MN-major box: 64 reduction rows of 64 elements
 
-enum class Form { kSingle, kSplit, kPair };
-
 // Blocks of 64 along the reduction that a stage of the ring holds. Two halve
 // the barrier traffic of a block, which bounds narrow tiles (pairs of width
 // 128: 221 -> 187 ns a block); the 48 KB blocks of wide single tiles leave no
@@ -411,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int m_total = S::kWeight ? p.groups * a.m_tiles : prefix[p.groups];
-  const uint32_t total = static_cast<uint32_t>(m_total) * a.n_tiles;  // below 2^31 (launch_mode)
+  const uint32_t total = static_cast<uint32_t>(m_total) * a.n_tiles;  // below 2^31 (plan_product)
   const uint32_t first_tile = blockIdx.x / split;
   const uint32_t step = kSplit ? 1u << 31 : gridDim.x / split;  // a split cluster has one tile (or none)
 
@@ -834,12 +832,6 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const TcA
   return launch_chained<kMode, kForm, true>(ta, tb, t, grid, cluster, s);
 }
 
-// How a product is cut up.
-struct Choice {
-  Form form;
-  int bn, split;
-};
-
 struct Problem {
   bool weight, across;  // weight mode; B lies across the reduction
   long long rows;  // tiled rows: of D in all groups, or of one group's D (weight mode)
@@ -876,8 +868,8 @@ double expected_tiles(const Problem& q, int tile) {
 // fill the last wave (skewed layer, 64 groups of 0 to 1920 rows out of 98304:
 // 256-wide pairs and single tiles 187 and 183 us, 192-wide pairs 217; 8 groups
 // of about 1000 rows 52, 57 and 61).
-Choice choose_tiles(const Problem& q, int sms) {
-  Choice best{Form::kSingle, kBN, 1};
+MatmulPlan choose_tiles(const Problem& q, int sms) {
+  MatmulPlan best{Form::kSingle, kBN, 1, 0};
   if (!q.weight && q.groups > 1 && q.n > kBN / 2 && expected_tiles(q, 256) * ((q.n + kBN - 1) / kBN) > sms) {
     if (q.rows >= 1024LL * q.groups) best.form = Form::kPair;
     return best;
@@ -890,7 +882,7 @@ Choice choose_tiles(const Problem& q, int sms) {
     const double time = waves * tile + once;
     if (time < least) {
       least = time;
-      best = {form, bn, split};
+      best = {form, bn, split, 0};
     }
   };
   for (int bn = kBN; bn >= 64; bn -= 32) {
@@ -909,14 +901,17 @@ Choice choose_tiles(const Problem& q, int sms) {
   return best;
 }
 
+Problem problem_of(MatmulMode mode, const MatmulArgs& a) {
+  const bool weight = mode == MatmulMode::kWgrad;
+  const int depth = weight ? (a.rows + a.groups - 1) / a.groups : a.k;
+  return {weight, mode != MatmulMode::kForward, weight ? a.m : a.rows, a.groups, a.n, (depth + kBK - 1) / kBK};
+}
+
 template <MatmulMode kMode>
-cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
+cudaError_t launch_mode(const MatmulPlan& choice, const MatmulArgs& a, int sms, cudaStream_t s) {
   using S = Shape<kMode>;
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
-  const int sms = device_sm_count();
-  const int depth = S::kWeight ? (a.rows + a.groups - 1) / a.groups : a.k;
-  const Problem q{S::kWeight, S::kAcrossB, S::kWeight ? a.m : a.rows, a.groups, a.n, (depth + kBK - 1) / kBK};
-  const Choice choice = choose_tiles(q, sms);
+  const int blocks = problem_of(kMode, a).blocks;
   const bool pair = choice.form == Form::kPair;
   const int tile_m = pair ? 256 : 128, b_cols = pair ? choice.bn / 2 : choice.bn;
   CUtensorMap ta, tb;
@@ -951,29 +946,35 @@ cudaError_t launch_mode(const MatmulArgs& a, cudaStream_t s) {
          load_map(&tb, a.b, fwd ? a.k : a.n, fwd ? a.n : a.k, a.ldb, a.groups, a.b_stride, fwd ? b_cols : 64);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const long long tiles = most_tiles(q, tile_m) * t.n_tiles;
-  if (tiles >= 1LL << 31) return cudaErrorInvalidValue;
+  const long long tiles = choice.tiles;
   switch (choice.form) {
     case Form::kPair:
-      return launch_tiles<kMode, Form::kPair>(ta, tb, t, q.blocks, 2 * std::min<long long>(tiles, sms / 2), 2, s);
+      return launch_tiles<kMode, Form::kPair>(ta, tb, t, blocks, 2 * std::min<long long>(tiles, sms / 2), 2, s);
     case Form::kSplit:
-      return launch_tiles<kMode, Form::kSplit>(ta, tb, t, (q.blocks + choice.split - 1) / choice.split, tiles * choice.split,
+      return launch_tiles<kMode, Form::kSplit>(ta, tb, t, (blocks + choice.split - 1) / choice.split, tiles * choice.split,
                                                choice.split, s);
     default:
-      return launch_tiles<kMode, Form::kSingle>(ta, tb, t, q.blocks, std::min<long long>(tiles, sms), 1, s);
+      return launch_tiles<kMode, Form::kSingle>(ta, tb, t, blocks, std::min<long long>(tiles, sms), 1, s);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
+MatmulPlan plan_matmul_tc(MatmulMode mode, const MatmulArgs& a, int sms) {
+  const Problem q = problem_of(mode, a);
+  MatmulPlan plan = choose_tiles(q, sms);
+  plan.tiles = most_tiles(q, plan.form == Form::kPair ? 256 : 128) * ((a.n + plan.bn - 1) / plan.bn);
+  return plan;
+}
+
+cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulPlan& plan, const MatmulArgs& a, int sms, cudaStream_t s) {
   switch (mode) {
     case MatmulMode::kForward:
-      return launch_mode<MatmulMode::kForward>(a, s);
+      return launch_mode<MatmulMode::kForward>(plan, a, sms, s);
     case MatmulMode::kDgrad:
-      return launch_mode<MatmulMode::kDgrad>(a, s);
+      return launch_mode<MatmulMode::kDgrad>(plan, a, sms, s);
     default:
-      return launch_mode<MatmulMode::kWgrad>(a, s);
+      return launch_mode<MatmulMode::kWgrad>(plan, a, sms, s);
   }
 }
 

@@ -196,16 +196,30 @@ struct MatmulArgs {
   int32_t* status;
   int vec, vec_out;        // fp32 path: operands' (outputs' and what is added to them) widths and strides are multiples of four
 };
+// How a product is cut up, from its sizes and the number of SMs alone.
+enum class Form {
+  kFewRows,  // matmul_rows.cu
+  kSingle,   // tiles of one CTA (bf16: 128 x bn, fp32: bn x bn)
+  kPair,     // bf16: 256 x bn tiles of CTA pairs
+  kSplit     // a cluster of `split` CTAs shares the reduction of a tile
+};
+struct MatmulPlan {
+  Form form;
+  int bn, split;
+  long long tiles;  // as many as there can be, however the rows fall to the groups (few rows: not set)
+};
 // matmul_simt.cu
-cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+MatmulPlan plan_matmul_f32(MatmulMode mode, const MatmulArgs& a, int sms);
+cudaError_t launch_matmul_f32(MatmulMode mode, const MatmulPlan& plan, const MatmulArgs& a, int sms, cudaStream_t s);
 // matmul_rows.cu: the forward for few rows a group, and whether a call is that (same demands as matmul_tc.cu)
-bool matmul_few_rows(const MatmulArgs& a);
-cudaError_t launch_matmul_rows(const MatmulArgs& a, cudaStream_t s);
+bool matmul_few_rows(const MatmulArgs& a, int sms);
+cudaError_t launch_matmul_rows(const MatmulArgs& a, int sms, cudaStream_t s);
 // the same in fp32 (any alignment)
 bool matmul_few_rows_f32(const MatmulArgs& a);
 cudaError_t launch_matmul_rows_f32(const MatmulArgs& a, cudaStream_t s);
-// matmul_tc.cu (strides and addresses on 16 bytes)
-cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulArgs& a, cudaStream_t s);
+// matmul_tc.cu (strides and addresses on 16 bytes; fewer than 2^31 tiles)
+MatmulPlan plan_matmul_tc(MatmulMode mode, const MatmulArgs& a, int sms);
+cudaError_t launch_matmul_tc(MatmulMode mode, const MatmulPlan& plan, const MatmulArgs& a, int sms, cudaStream_t s);
 // matmul_simt.cu; status: NULL if a product of the same call reports the offsets
 cudaError_t launch_column_sums(int dtype, const void* dy, long long ld, const int32_t* offsets, int groups, int rows,
                                int n, float* out, int32_t* status, bool vec, cudaStream_t s);

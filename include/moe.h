@@ -449,7 +449,8 @@ MOE_API int32_t moe_debug_stall_next_gemms(int32_t n);
  * ones on tensor cores. No workspace. Deterministic.
  * No other operand may overlap an output.
  * Limits: 1 <= groups <= MOE_MAX_E, n, k >= 1, n * groups < 2^31, rows, n and
- * k at most 2^31 - 1025 (bf16: n and k at most 2^26).
+ * k at most 2^31 - 1025 (bf16: n and k at most 2^26, and fewer than 2^31
+ * tiles of 128 or 256 rows of a group by 64 to 256 columns).
  * Errors: MOE_ERR_INVALID_ARG (NULL, negative sizes, a stride below its
  * width, unknown act or dtype), MOE_ERR_UNSUPPORTED (limits, a pointer off 16
  * bytes (bias, dw, dbias, offsets: 4), a bf16 stride that is no multiple of

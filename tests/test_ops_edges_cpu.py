@@ -64,3 +64,18 @@ def test_memory_for_another_stream(monkeypatch):
     assert log == ["enter", "empty", "exit", ("record", "current")]
     monkeypatch.setattr(torch, "empty", empty)
     assert _lib._empty((2, 3), torch.float32, "cpu", None).shape == (2, 3)
+
+
+PTR = 1 << 20  # an aligned address that no refused call reads
+
+
+def test_products_of_too_many_tiles_are_refused(L):
+    """bf16 tiles are counted in 32 bits; the documented answer comes before any CUDA call."""
+    most = (1 << 31) - 1025
+    wide = M.MoeGemmConfig(rows=most, n=1 << 26, k=8, groups=1, dtype=M.MOE_DTYPE_BF16)
+    deep = M.MoeGemmConfig(rows=most, n=8, k=1 << 26, groups=1, dtype=M.MOE_DTYPE_BF16)
+    both = M.MoeGemmConfig(rows=128, n=1 << 26, k=1 << 26, groups=1, dtype=M.MOE_DTYPE_BF16)
+    U = M.MOE_ERR_UNSUPPORTED
+    assert L.moe_linear(wide, PTR, PTR, None, None, None, PTR, None, None) == U
+    assert L.moe_linear_dgrad(deep, PTR, PTR, None, None, PTR, None, None) == U
+    assert L.moe_linear_wgrad(both, PTR, PTR, PTR, None, None, None) == U
