@@ -26,9 +26,11 @@ struct Uses {
   int64_t r_width, z_width;  // widths of residual and z rows, 0 if the call has none
 };
 
+constexpr int64_t kFar = 1LL << 36;  // elements: tensor maps hold strides of less than 2^40 bytes
+
 bool stride_ok(int64_t ld, int64_t width, bool bf16, int& rc) {
   if (ld < width) rc = MOE_ERR_INVALID_ARG;
-  else if (bf16 && ld % 8 != 0) rc = MOE_ERR_UNSUPPORTED;
+  else if (ld > kFar || (bf16 && ld % 8 != 0)) rc = MOE_ERR_UNSUPPORTED;
   return rc == MOE_OK;
 }
 
@@ -54,7 +56,6 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   if (c.ldy == 0) c.ldy = c.n;
   if (c.ldr == 0) c.ldr = u.r_width;
   if (c.ldz == 0) c.ldz = u.z_width;
-  if (c.w_stride == 0 || c.groups == 1) c.w_stride = c.ldw * c.n;
   const bool bf16 = c.dtype == MOE_DTYPE_BF16;
   p.rc = MOE_OK;
   if (u.x && !stride_ok(c.ldx, c.k, bf16, p.rc)) return p;
@@ -63,12 +64,15 @@ Product check(const moe_gemm_config* cfg, bool dense, const Uses& u) {
   if (u.z_width && !stride_ok(c.ldz, u.z_width, bf16, p.rc)) return p;
   if (u.w) {
     if (!stride_ok(c.ldw, c.k, bf16, p.rc)) return p;
-    if (c.groups > 1 && !stride_ok(c.w_stride, (c.n - 1) * c.ldw + c.k, bf16, p.rc)) return p;
+    if (c.groups == 1) {
+      c.w_stride = c.ldw;  // leads nowhere
+    } else if (c.n - 1 > kFar / c.ldw) {  // no group stride is long enough
+      p.rc = MOE_ERR_UNSUPPORTED;
+    } else {
+      if (c.w_stride == 0) c.w_stride = c.ldw * c.n;
+      stride_ok(c.w_stride, (c.n - 1) * c.ldw + c.k, bf16, p.rc);
+    }
   }
-  // tensor maps hold strides of up to 2^40 bytes
-  const int64_t far = 1LL << 36;
-  if (c.ldx > far || c.ldw > far || c.ldy > far || c.ldr > far || c.ldz > far || c.w_stride > far)
-    p.rc = MOE_ERR_UNSUPPORTED;
   return p;
 }
 

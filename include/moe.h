@@ -223,7 +223,8 @@ typedef struct moe_config {
 /* A free product's shapes. The row strides are in elements; 0 stands for
  * contiguous rows. bf16 strides are multiples of 8 (rows start on 16 bytes;
  * the widths n and k may be odd inside them), fp32 strides are free. A stride
- * is at least the width of its rows. */
+ * is at least the width of its rows and at most 2^36. Strides of operands that
+ * a call does not have are not looked at. */
 typedef struct moe_gemm_config {
   int32_t rows;     /* rows of x, y, dy, dx, residual, z and preact, all groups together */
   int32_t n;        /* output features: columns of y and dy, rows of each W */

@@ -232,3 +232,21 @@ def test_dropout_of_the_widest_rows(cols):
                                       (seed, 0)), axis=1).reshape(-1)[:last - first]
         want = torch.from_numpy((words >= 1 << 31).astype(np.float64)) * 2
         assert torch.equal(y[0, first:last].cpu().double(), want), first
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_strides_of_absent_operands_do_not_matter(dt):
+    """A bias gradient beside a dw that nobody could hold, and far strides of operands that the call does not have."""
+    g = torch.Generator().manual_seed(7)
+    n = k = 1 << 19
+    dy = torch.randint(-3, 4, (5, n), generator=g).to(dt).to(DEV)
+    x = torch.zeros((5, k), dtype=dt, device=DEV)
+    db = torch.full((n,), math.nan, device=DEV)
+    cfg = M.MoeGemmConfig(rows=5, n=n, k=k, groups=1, dtype=CODE[dt])
+    assert M.lib().moe_linear_wgrad(cfg, dy.data_ptr(), x.data_ptr(), None, db.data_ptr(), None, stream()) == M.MOE_OK
+    assert torch.equal(db, dy.float().sum(0))
+    x, w = torch.ones((5, 64), dtype=dt, device=DEV), torch.ones((8, 64), dtype=dt, device=DEV)
+    y = torch.zeros((5, 8), dtype=dt, device=DEV)
+    cfg = M.MoeGemmConfig(rows=5, n=8, k=64, groups=1, dtype=CODE[dt], ldr=1 << 40, ldz=1 << 40, w_stride=1 << 40)
+    assert M.lib().moe_linear(cfg, x.data_ptr(), w.data_ptr(), None, None, None, y.data_ptr(), None, stream()) == M.MOE_OK
+    assert bool((y == 64).all())

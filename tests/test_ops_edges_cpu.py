@@ -79,3 +79,13 @@ def test_products_of_too_many_tiles_are_refused(L):
     assert L.moe_linear(wide, PTR, PTR, None, None, None, PTR, None, None) == U
     assert L.moe_linear_dgrad(deep, PTR, PTR, None, None, PTR, None, None) == U
     assert L.moe_linear_wgrad(both, PTR, PTR, PTR, None, None, None) == U
+
+
+@pytest.mark.parametrize("kw", [dict(ldw=1 << 36, n=1 << 29), dict(ldw=1 << 36, n=(1 << 30) - 1),
+                                dict(ldw=1 << 36, n=1 << 28, w_stride=1 << 36), dict(ldw=(1 << 62) + 8, n=5),
+                                dict(ldw=1 << 37, n=8), dict(n=8, w_stride=1 << 37)])
+def test_weight_strides_are_checked_without_overflow(L, kw):
+    """Strides whose product with n leaves 64 bits once looked like short ones."""
+    cfg = M.MoeGemmConfig(rows=8, k=32, groups=2, dtype=M.MOE_DTYPE_F32, **kw)
+    assert L.moe_grouped_gemm(cfg, PTR, PTR, PTR, None, None, None, PTR, None, None) == M.MOE_ERR_UNSUPPORTED
+    assert L.moe_grouped_gemm_dgrad(cfg, PTR, PTR, PTR, None, None, PTR, None, None) == M.MOE_ERR_UNSUPPORTED
