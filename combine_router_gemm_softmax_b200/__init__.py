@@ -19,6 +19,7 @@ tensors into its entry points:
                            and residual (_dgrad, _wgrad: its gradients)
     moe_linear             the same for one dense weight (_dgrad, _wgrad)
     moe_act_backward       gradient through an activation alone
+    moe_product_form_used  how a product of given sizes is cut up (host only)
     moe_dropout            residual dropout, the mask drawn from a counter (its own backward)
     moe_unpermute_combine_dropout  combine, dropout and residual in one pass
 """
@@ -37,4 +38,5 @@ from ._lib import (  # noqa: F401
     moe_mxfp8_quantize, moe_mxfp8_weights_size, moe_pack_weights_mxfp8, mx_counters, mxfp8_scale_bytes,
     MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_STATUS_BAD_OFFSETS, MoeGemmConfig,
     moe_act_backward, moe_dropout, moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_linear,
-    moe_linear_dgrad, moe_linear_wgrad, moe_unpermute_combine_dropout)
+    moe_linear_dgrad, moe_linear_wgrad, moe_unpermute_combine_dropout, MOE_FORM_FEW_ROWS, MOE_FORM_PAIR,
+    MOE_FORM_SINGLE, MOE_FORM_SPLIT, moe_product_form_used)

@@ -21,6 +21,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
 MOE_STATUS_NAN_LOGIT, MOE_STATUS_BAD_ROUTE, MOE_STATUS_TIMEOUT = 1, 2, 4
 MOE_STATUS_MX_SATURATED, MOE_STATUS_MX_UNDERFLOW, MOE_STATUS_BAD_OFFSETS = 8, 16, 32
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU = 0, 1, 2, 3, 4
+MOE_PRODUCT_FORWARD, MOE_PRODUCT_DGRAD, MOE_PRODUCT_WGRAD = 0, 1, 2
+MOE_FORM_FEW_ROWS, MOE_FORM_SINGLE, MOE_FORM_PAIR, MOE_FORM_SPLIT = 0, 1, 2, 3
 MOE_PRECISION_BF16, MOE_PRECISION_MXFP8 = 0, 1
 MOE_COMBINE_AUTO, MOE_COMBINE_SEPARATE, MOE_COMBINE_FUSED = 0, 1, 2
 MOE_PREACT_RECOMPUTE, MOE_PREACT_SAVE = 0, 1
@@ -38,7 +40,7 @@ EXPORTED = ("moe_workspace_size", "moe_status_string", "moe_version", "moe_pack_
             "moe_layer_backward", "moe_mxfp8_quantize", "moe_mxfp8_weights_size", "moe_pack_weights_mxfp8",
             "moe_debug_stall_next_gemms", "moe_gemm_tiles_used", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
             "moe_grouped_gemm_wgrad", "moe_linear", "moe_linear_dgrad", "moe_linear_wgrad", "moe_act_backward",
-            "moe_dropout", "moe_unpermute_combine_dropout")
+            "moe_dropout", "moe_unpermute_combine_dropout", "moe_product_form_used")
 
 
 class MoeError(RuntimeError):
@@ -108,6 +110,7 @@ _SIGS = {
     "moe_linear_wgrad": (I32, [GCFG, P, P, P, P, P, P]),
     "moe_act_backward": (I32, [GCFG, P, P, P, P]),
     "moe_dropout": (I32, [I32, I32, I32, P, I64, P, I64, P, I64, F64, P, U64, P]),
+    "moe_product_form_used": (I32, [GCFG, I32, I32, P]),
     "moe_unpermute_combine_dropout": (I32, [CFG, P, P, P, P, F64, P, U64, P, P]),
 }
 
@@ -699,6 +702,22 @@ def _given(offsets):
     if offsets is None:
         raise TypeError("offsets: expected a torch.Tensor")
     return offsets
+
+
+_PRODUCTS = {"forward": MOE_PRODUCT_FORWARD, "dgrad": MOE_PRODUCT_DGRAD, "wgrad": MOE_PRODUCT_WGRAD}
+
+
+def moe_product_form_used(product, rows, n, k, groups=1, dtype=torch.bfloat16, sms=148):
+    """How a product ("forward", "dgrad" or "wgrad") of these sizes is cut up on
+    a device of `sms` SMs: (MOE_FORM_*, columns of a tile, CTAs that share a
+    reduction). Host only."""
+    if product not in _PRODUCTS:
+        raise ValueError(f"product: {product!r} is none of {', '.join(_PRODUCTS)}")
+    wide = [(v + 7) // 8 * 8 for v in (k, n)]  # rows on 16 bytes, as bf16 operands have them
+    cfg = MoeGemmConfig(rows, n, k, groups, _GEMM_DTYPES[dtype], MOE_ACT_NONE, wide[0], wide[0], 0, wide[1], 0, 0)
+    form = (ctypes.c_int32 * 3)()
+    _rc("moe_product_form_used", lib().moe_product_form_used(ctypes.byref(cfg), _PRODUCTS[product], sms, form))
+    return tuple(form)
 
 
 def moe_act_backward(dy, z, act, dz=None, stream=None):

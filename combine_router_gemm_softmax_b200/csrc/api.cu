@@ -517,7 +517,7 @@ using namespace moe;
 
 extern "C" {
 
-int32_t moe_version(void) { return (1 << 16) | 3; }
+int32_t moe_version(void) { return (1 << 16) | 4; }
 
 int32_t moe_gemm_tiles_used(const moe_config* cfg, int32_t* tiles) {
   if (tiles == nullptr) return MOE_ERR_INVALID_ARG;

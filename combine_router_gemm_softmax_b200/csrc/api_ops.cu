@@ -83,11 +83,14 @@ MatmulPlan plan_product(int dtype, MatmulMode mode, const MatmulArgs& a, int sms
   return f32 ? plan_matmul_f32(mode, a, sms) : plan_matmul_tc(mode, a, sms);
 }
 
+// Products of 2^31 tiles or more leave the bf16 tiles' 32-bit indices.
+bool too_many(int dtype, const MatmulPlan& plan) { return dtype == MOE_DTYPE_BF16 && plan.tiles >= 1LL << 31; }
+
 int launch_product(int dtype, MatmulMode mode, const MatmulArgs& a, cudaStream_t s) {
   const bool f32 = dtype == MOE_DTYPE_F32;
   const int sms = device_sm_count();
   const MatmulPlan plan = plan_product(dtype, mode, a, sms);
-  if (plan.tiles >= 1LL << 31 && !f32) return MOE_ERR_UNSUPPORTED;  // the tiles' 32-bit indices
+  if (too_many(dtype, plan)) return MOE_ERR_UNSUPPORTED;
   if (plan.form == Form::kFewRows) return rc_of(f32 ? launch_matmul_rows_f32(a, s) : launch_matmul_rows(a, sms, s));
   return rc_of(f32 ? launch_matmul_f32(mode, plan, a, sms, s) : launch_matmul_tc(mode, plan, a, sms, s));
 }
@@ -212,6 +215,30 @@ int32_t moe_linear_dgrad(const moe_gemm_config* cfg, const void* dy, const void*
 int32_t moe_linear_wgrad(const moe_gemm_config* cfg, const void* dy, const void* x, float* dw, float* dbias,
                          int32_t* status_dev, moe_stream_t stream) {
   return wgrad(cfg, true, dy, nullptr, x, dw, dbias, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_product_form_used(const moe_gemm_config* cfg, int32_t product, int32_t sms, int32_t* form) {
+  if (form == nullptr || sms <= 0 || product < MOE_PRODUCT_FORWARD || product > MOE_PRODUCT_WGRAD)
+    return MOE_ERR_INVALID_ARG;
+  const bool weight = product == MOE_PRODUCT_WGRAD;
+  const Product p = check(cfg, false, {true, !weight, true, 0, 0});
+  if (p.rc != MOE_OK) return p.rc;
+  const moe_gemm_config& c = p.c;
+  MatmulArgs a{};
+  a.groups = c.groups, a.rows = c.rows, a.m = c.n;
+  a.n = product == MOE_PRODUCT_FORWARD ? c.n : c.k, a.k = product == MOE_PRODUCT_FORWARD ? c.k : c.n;
+  const MatmulMode mode = product == MOE_PRODUCT_FORWARD ? MatmulMode::kForward
+                          : weight                       ? MatmulMode::kWgrad
+                                                         : MatmulMode::kDgrad;
+  const MatmulPlan plan = plan_product(c.dtype, mode, a, sms);
+  if (too_many(c.dtype, plan)) return MOE_ERR_UNSUPPORTED;
+  form[0] = plan.form == Form::kFewRows  ? MOE_FORM_FEW_ROWS
+            : plan.form == Form::kSingle ? MOE_FORM_SINGLE
+            : plan.form == Form::kPair   ? MOE_FORM_PAIR
+                                         : MOE_FORM_SPLIT;
+  form[1] = plan.bn;
+  form[2] = plan.split;
+  return MOE_OK;
 }
 
 int32_t moe_act_backward(const moe_gemm_config* cfg, const void* dy, const void* z, void* dz, moe_stream_t stream) {

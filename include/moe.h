@@ -193,6 +193,18 @@ extern "C" {
 #define MOE_ACT_GELU_TANH 3
 #define MOE_ACT_SILU      4
 
+/* The products of moe_grouped_gemm (moe_linear), _dgrad and _wgrad, and how
+ * moe_product_form_used says that one is cut up: for few rows a group, in
+ * tiles of one CTA, in tiles of CTA pairs, or in tiles whose reduction a
+ * cluster of CTAs shares. */
+#define MOE_PRODUCT_FORWARD 0
+#define MOE_PRODUCT_DGRAD   1
+#define MOE_PRODUCT_WGRAD   2
+#define MOE_FORM_FEW_ROWS 0
+#define MOE_FORM_SINGLE   1
+#define MOE_FORM_PAIR     2
+#define MOE_FORM_SPLIT    3
+
 #define MOE_OP_ROUTE       0
 #define MOE_OP_PERMUTE     1
 #define MOE_OP_GROUPED_FFN 2
@@ -494,6 +506,15 @@ MOE_API int32_t moe_linear_dgrad(const moe_gemm_config* cfg, const void* dy, con
                                  const void* residual, void* dx, int32_t* status_dev, moe_stream_t stream);
 MOE_API int32_t moe_linear_wgrad(const moe_gemm_config* cfg, const void* dy, const void* x, float* dw, float* dbias,
                                  int32_t* status_dev, moe_stream_t stream);
+
+/* moe_product_form_used -- writes to form[0] the MOE_FORM_* that a product
+ * (MOE_PRODUCT_*) of cfg takes on a device of `sms` SMs, to form[1] its tiles'
+ * columns (0 for few rows) and to form[2] the CTAs that share a reduction.
+ * rows, n, k, groups and dtype decide; bf16 reductions longer than 16384
+ * elements (512 rows in wgrad) besides leave their accumulators on the way.
+ * Returns MOE_OK, or what the product itself returns for such a cfg; form is
+ * then untouched. Host only: no GPU work, no CUDA call. */
+MOE_API int32_t moe_product_form_used(const moe_gemm_config* cfg, int32_t product, int32_t sms, int32_t* form);
 
 /* moe_act_backward -- dz[r, j] = dy[r, j] act'(z[r, j]) over [rows, n], for an
  * activation whose output no further product consumes (else

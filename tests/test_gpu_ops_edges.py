@@ -8,6 +8,7 @@ import torch
 
 import combine_router_gemm_softmax_b200 as M
 from oracle import ops as R
+from ops_forms import FIRST, FORMS, LONG, form_of, name_of, rows_of
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -86,14 +87,8 @@ def test_activations_far_from_zero(act, dt):
     assert torch.equal(v, pos * z[0, :14].cpu())
 
 
-LONG = [  # (rows of each group, length of the reduction, width): few rows, few tiles, many tiles, ragged groups
-    ([4], 1 << 20, 16), ([3], (1 << 16) + 24, 9600), ([300], (1 << 19) + 8, 264), ([2048], 1 << 17, 2048),
-    ([200, 0, 130, 7, 500], (1 << 18) + 72, 328), ([16384], 3 * 16384 + 64, 136),
-]
-
-
 @pytest.mark.parametrize("dgrad", [False, True], ids=["forward", "dgrad"])
-@pytest.mark.parametrize("sizes,length,width", LONG)
+@pytest.mark.parametrize("sizes,length,width", [c[:3] for c in LONG])
 def test_long_reductions_are_not_biased(sizes, length, width, dgrad):
     """bf16 products of one sign over long reductions. Tensor cores truncate when they add, so that the error of one
     accumulator grows with the length (7e-4 at 2^20); kept to 16384 elements, 1024 steps of 16, it is at most
@@ -250,3 +245,91 @@ def test_strides_of_absent_operands_do_not_matter(dt):
     cfg = M.MoeGemmConfig(rows=5, n=8, k=64, groups=1, dtype=CODE[dt], ldr=1 << 40, ldz=1 << 40, w_stride=1 << 40)
     assert M.lib().moe_linear(cfg, x.data_ptr(), w.data_ptr(), None, None, None, y.data_ptr(), None, stream()) == M.MOE_OK
     assert bool((y == 64).all())
+
+
+# ------------------------------------------------------------------ every form, exactly
+
+def integers(shape, dt, g, pad=0, most=2):
+    """Whole numbers of up to `most` either way; with pad, rows that lie apart with NaN between them."""
+    t = torch.randint(-most, most + 1, shape, generator=g, device=DEV).to(dt)
+    if not pad:
+        return t
+    wide = torch.full((*shape[:-1], (shape[-1] + 7) // 8 * 8 + pad), math.nan, dtype=dt, device=DEV)
+    wide[..., :shape[-1]] = t
+    return wide[..., :shape[-1]]
+
+
+def exactly(got, want, what):
+    """want: the exact result in fp32 (whole numbers below 2^24); got: that, rounded once."""
+    want = want.to(got.dtype)
+    if not torch.equal(got, want):
+        bad = (got != want) | got.isnan()
+        at = torch.nonzero(bad)
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} wrong, first at {at[0].tolist()}, last at "
+                             f"{at[-1].tolist()}: {float(got[bad][0])}, not {float(want[bad][0])}")
+
+
+def product_setup(case):
+    _, dt, sizes, n, k, pad, form, _ = case
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert form_of(case, sms)[0] == form
+    g = torch.Generator(device=DEV).manual_seed(n * 31 + k)
+    dense = isinstance(sizes, int)
+    ends = [0, sizes] if dense else [FIRST + sum(sizes[:e]) for e in range(len(sizes) + 1)]
+    rows, E = rows_of(sizes), len(ends) - 1
+    o = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    x, dy = integers((rows, k), dt, g, pad), integers((rows, n), dt, g, pad)
+    for t in (x, dy):  # rows of no group: nothing may see them
+        t[:ends[0]], t[ends[-1]:] = math.nan, math.nan
+    return g, dense, ends, rows, E, o, x, dy
+
+
+@pytest.mark.parametrize("case", FORMS, ids=name_of)
+def test_every_form_exactly(case):
+    """Products of small whole numbers, whose sums every order and every accumulator holds exactly: one element that
+    is missing, read twice or of another group, at any length, makes a difference."""
+    product, dt, sizes, n, k, pad = case[:6]
+    g, dense, ends, rows, E, o, x, dy = product_setup(case)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    inside = slice(ends[0], ends[-1])
+    if product == "wgrad":
+        dw, db = torch.full((E, n, k), math.nan, device=DEV), torch.full((E, n), math.nan, device=DEV)
+        if dense:
+            M.moe_linear_wgrad(dy, x, dw=dw[0], dbias=db[0], status=status)
+        else:
+            M.moe_grouped_gemm_wgrad(dy, o, x, dw=dw, dbias=db, status=status)
+        for e, (a, b) in R.groups(ends):
+            exactly(dw[e], dy[a:b].float().T @ x[a:b].float(), f"dw {e}")
+            exactly(db[e], dy[a:b].float().sum(0), f"dbias {e}")
+        assert int(status.item()) == 0
+        return
+    w = integers((E, n, k), dt, g, pad)
+    width = n if product == "forward" else k
+    res = integers((rows, width), dt, g, pad)
+    out = integers((rows, width), dt, g, pad).fill_(5.0)
+    if product == "forward":
+        bias = torch.randint(-9, 10, (E, n), generator=g, device=DEV).float()
+        pre = integers((rows, width), dt, g, pad).fill_(5.0)
+        if dense:
+            M.moe_linear(x, w[0], bias=bias[0], act="relu", residual=res, preact=pre, y=out, status=status)
+        else:
+            M.moe_grouped_gemm(x, o, w, bias=bias, act="relu", residual=res, preact=pre, y=out, status=status)
+    else:
+        z = integers((rows, k), dt, g, pad, 1)  # relu's slope: one or zero
+        if dense:
+            M.moe_linear_dgrad(dy, w[0], z=z, act="relu", residual=res, dx=out, status=status)
+        else:
+            M.moe_grouped_gemm_dgrad(dy, o, w, z=z, act="relu", residual=res, dx=out, status=status)
+    assert int(status.item()) == 0
+    for e, (a, b) in R.groups(ends):
+        if product == "forward":
+            u = x[a:b].float() @ w[e].float().T + bias[e]
+            exactly(pre[a:b], u, f"preact {e}")
+            exactly(out[a:b], u.clamp(min=0) + res[a:b].float(), f"y {e}")
+        else:
+            exactly(out[a:b], (z[a:b] > 0) * (dy[a:b].float() @ w[e].float()) + res[a:b].float(), f"dx {e}")
+    outside = torch.ones(rows, dtype=torch.bool, device=DEV)
+    outside[inside] = False
+    assert bool((out[outside] == 5).all())
+    if product == "forward":
+        assert bool((pre[outside] == 5).all())

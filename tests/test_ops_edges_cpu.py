@@ -1,6 +1,7 @@
 """The operators around the layer on the CPU: limits at their edges, what the
 binding makes for a call, and which kernel form a call takes."""
 import ast
+import ctypes
 import inspect
 
 import pytest
@@ -8,6 +9,7 @@ import torch
 
 import combine_router_gemm_softmax_b200 as M
 from combine_router_gemm_softmax_b200 import _lib
+from ops_forms import FORMS, LONG, form_of, name_of
 
 
 @pytest.fixture(scope="module")
@@ -89,3 +91,49 @@ def test_weight_strides_are_checked_without_overflow(L, kw):
     cfg = M.MoeGemmConfig(rows=8, k=32, groups=2, dtype=M.MOE_DTYPE_F32, **kw)
     assert L.moe_grouped_gemm(cfg, PTR, PTR, PTR, None, None, None, PTR, None, None) == M.MOE_ERR_UNSUPPORTED
     assert L.moe_grouped_gemm_dgrad(cfg, PTR, PTR, PTR, None, None, PTR, None, None) == M.MOE_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ forms
+
+@pytest.mark.parametrize("case", FORMS, ids=name_of)
+def test_cases_take_their_form(L, case):
+    """On a B200's 148 SMs. A change of the rule that moves a case has to bring another one for its form."""
+    assert form_of(case, 148)[:2] == case[6:]
+
+
+def test_long_cases_take_every_form(L):
+    have = set()
+    for sizes, length, width, forward, dgrad in LONG:
+        assert M.moe_product_form_used("forward", sum(sizes), width, length, len(sizes))[0] == forward
+        assert M.moe_product_form_used("dgrad", sum(sizes), length, width, len(sizes))[0] == dgrad
+        have |= {("forward", forward), ("dgrad", dgrad)}
+    tiles = {M.MOE_FORM_SINGLE, M.MOE_FORM_PAIR, M.MOE_FORM_SPLIT}
+    assert have == {(p, f) for p in ("forward", "dgrad") for f in tiles} | {("forward", M.MOE_FORM_FEW_ROWS)}
+
+
+def test_cases_cover_every_form(L):
+    have = {(c[0], c[1], isinstance(c[2], int), c[6]) for c in FORMS}
+    for dense in (True, False):
+        for product in ("forward", "dgrad", "wgrad"):
+            for dt in (torch.bfloat16, torch.float32):
+                forms = {M.MOE_FORM_SINGLE, M.MOE_FORM_SPLIT}
+                if dt == torch.bfloat16:
+                    forms.add(M.MOE_FORM_PAIR)
+                # few rows in fp32 over groups: tests/test_gpu_ops.py ("one_row_each", "few")
+                if product == "forward" and (dense or dt == torch.bfloat16):
+                    forms.add(M.MOE_FORM_FEW_ROWS)
+                assert {(product, dt, dense, f) for f in forms} <= have
+
+
+def test_form_query_refuses(L):
+    I, U = M.MOE_ERR_INVALID_ARG, M.MOE_ERR_UNSUPPORTED
+    form = (ctypes.c_int32 * 3)(7, 7, 7)
+    cfg = M.MoeGemmConfig(rows=8, n=16, k=32, groups=2, dtype=M.MOE_DTYPE_BF16)
+    for args in ((None, 0, 148, form), (cfg, 3, 148, form), (cfg, -1, 148, form), (cfg, 0, 0, form), (cfg, 0, 148, None)):
+        assert L.moe_product_form_used(*args) == I
+    assert L.moe_product_form_used(M.MoeGemmConfig(rows=8, n=16, k=31, groups=2), 0, 148, form) == U
+    assert L.moe_product_form_used(M.MoeGemmConfig(rows=(1 << 31) - 1025, n=1 << 26, k=8, groups=1), 0, 148, form) == U
+    assert list(form) == [7, 7, 7]
+    assert L.moe_product_form_used(cfg, 0, 148, form) == M.MOE_OK and list(form) == [M.MOE_FORM_FEW_ROWS, 0, 1]
+    with pytest.raises(ValueError, match="product"):
+        M.moe_product_form_used("backward", 8, 16, 32)
