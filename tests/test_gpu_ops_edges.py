@@ -333,3 +333,23 @@ def test_every_form_exactly(case):
     assert bool((out[outside] == 5).all())
     if product == "forward":
         assert bool((pre[outside] == 5).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("sizes,n,k", [([700001], 8, 8), ([300000, 0, 1, 400000], 8, 8), ([20000], 160, 72),
+                                       ([20000, 3, 0, 40001], 136, 264)])
+def test_long_sums_of_rows_miss_none(dt, sizes, n, k):
+    """Weight and bias gradients over very many rows, exactly (sums of whole numbers below 2^24): a bound that grows
+    with the rows would let whole blocks of them go missing."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    ends = [FIRST + sum(sizes[:e]) for e in range(len(sizes) + 1)]
+    rows, E = rows_of(sizes), len(sizes)
+    o = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    dy, x = integers((rows, n), dt, g), integers((rows, k), dt, g)
+    for t in (x, dy):
+        t[:ends[0]], t[ends[-1]:] = math.nan, math.nan
+    db = torch.full((E, n), math.nan, device=DEV)
+    dw = M.moe_grouped_gemm_wgrad(dy, o, x, dbias=db)
+    for e, (a, b) in R.groups(ends):
+        exactly(dw[e], (dy[a:b].double().T @ x[a:b].double()).float(), f"dw {e}")
+        exactly(db[e], dy[a:b].double().sum(0).float(), f"dbias {e}")
