@@ -353,3 +353,34 @@ def test_long_sums_of_rows_miss_none(dt, sizes, n, k):
     for e, (a, b) in R.groups(ends):
         exactly(dw[e], (dy[a:b].double().T @ x[a:b].double()).float(), f"dw {e}")
         exactly(db[e], dy[a:b].double().sum(0).float(), f"dbias {e}")
+
+
+STALLS = [c for c in FORMS if c[1] == BF16 and c[6] != M.MOE_FORM_FEW_ROWS and c[2] in (
+    331, 12293, [70, 0, 200, 1, 33, 19], 16381, [130, 0, 7], 8193, [18000, 14742], [2049, 1, 4099])]
+
+
+@pytest.mark.parametrize("case", STALLS, ids=name_of)
+def test_a_wait_that_runs_out_in_every_form(case):
+    """The tiles' timeout path in the forms named by the case (forward single, pair and split; dgrad pair and split;
+    wgrad pair and split, their zeroed rows included): the MMA warp waits on a barrier that nothing signals until its
+    limit, the status says so, and the next call is right."""
+    product, dt, sizes, n, k, pad = case[:6]
+    g, dense, ends, rows, E, o, x, dy = product_setup(case)
+    w = integers((E, n, k), dt, g, pad)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    call = {"forward": lambda: M.moe_grouped_gemm(x, o, w, status=status)[ends[0]:ends[-1]],
+            "dgrad": lambda: M.moe_grouped_gemm_dgrad(dy, o, w, status=status)[ends[0]:ends[-1]],
+            "wgrad": lambda: M.moe_grouped_gemm_wgrad(dy, o, x, status=status)}[product]
+    ref = call().clone()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert M.lib().moe_debug_stall_next_gemms(1) == M.MOE_OK
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        M.lib().moe_debug_stall_next_gemms(0)
+    assert int(status.item()) == M.MOE_STATUS_TIMEOUT
+    status.zero_()
+    assert torch.equal(call(), ref)
+    assert int(status.item()) == 0

@@ -137,3 +137,10 @@ def test_form_query_refuses(L):
     assert L.moe_product_form_used(cfg, 0, 148, form) == M.MOE_OK and list(form) == [M.MOE_FORM_FEW_ROWS, 0, 1]
     with pytest.raises(ValueError, match="product"):
         M.moe_product_form_used("backward", 8, 16, 32)
+
+
+def test_stalled_cases_take_every_tiled_form(L):
+    from test_gpu_ops_edges import STALLS
+    assert {(c[0], c[6]) for c in STALLS} >= {(p, f) for p, f in (
+        ("forward", M.MOE_FORM_SINGLE), ("forward", M.MOE_FORM_PAIR), ("forward", M.MOE_FORM_SPLIT),
+        ("dgrad", M.MOE_FORM_PAIR), ("dgrad", M.MOE_FORM_SPLIT), ("wgrad", M.MOE_FORM_PAIR), ("wgrad", M.MOE_FORM_SPLIT))}
