@@ -509,7 +509,11 @@ def _strided(t, shape, dtype, index, name):
     axis) and returns its address and row stride; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+    try:
+        wrong = t.shape != shape or t.dtype is not dtype or t.get_device() != index
+    except AttributeError:  # no tensor
+        wrong = True
+    if wrong:
         _refuse(t, shape, dtype, index, name)
     st = t.stride()
     width = shape[-1]
@@ -530,11 +534,24 @@ def _plain(t, shape, dtype, index, name):
     """Address of a contiguous tensor of this shape; None for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+    try:
+        wrong = t.shape != shape or t.dtype is not dtype or t.get_device() != index
+    except AttributeError:  # no tensor
+        wrong = True
+    if wrong:
         _refuse(t, shape, dtype, index, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
+
+
+def _axes(t, dims, name):
+    try:
+        have = t.dim()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
+    if have != dims:
+        raise ValueError(f"{name}: {have} axes, not {dims}")
 
 
 def _first(t, dims, name):
@@ -544,8 +561,7 @@ def _first(t, dims, name):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name}: must be on a CUDA device")
-    if t.dim() != dims:
-        raise ValueError(f"{name}: {t.dim()} axes, not {dims}")
+    _axes(t, dims, name)
     try:
         return index, _GEMM_DTYPES[t.dtype]
     except KeyError:
@@ -579,8 +595,7 @@ def _weights(w, groups, n, k, dtype, index):
 
 def _forward(fn, dims, x, offsets, w, bias, act, residual, preact, y, status, stream):
     dev, dt = _first(x, 2, "x")
-    if w.dim() != dims:
-        raise ValueError(f"w: {w.dim()} axes, not {dims}")
+    _axes(w, dims, "w")
     rows, k = x.shape
     shape = w.shape
     n = shape[-2]
@@ -607,8 +622,7 @@ def _forward(fn, dims, x, offsets, w, bias, act, residual, preact, y, status, st
 
 def _dgrad(fn, dims, dy, offsets, w, z, act, residual, dx, status, stream):
     dev, dt = _first(dy, 2, "dy")
-    if w.dim() != dims:
-        raise ValueError(f"w: {w.dim()} axes, not {dims}")
+    _axes(w, dims, "w")
     rows, n = dy.shape
     k = w.shape[-1]
     groups = w.shape[0] if dims == 3 else 1
@@ -665,20 +679,26 @@ def moe_grouped_gemm(x, offsets, w, bias=None, act="none", residual=None, preact
     share memory with an output. stream: where the call runs (default: the
     device's current one), after whatever made its arguments; other streams
     wait for it before they read its outputs. Returns y."""
-    return _forward("moe_grouped_gemm", 3, x, _given(offsets), w, bias, act, residual, preact, y, status, stream)
+    return _forward("moe_grouped_gemm", 3, x, _required(offsets, "offsets"), w, bias, act, residual, preact, y, status,
+                    stream)
 
 
 def moe_grouped_gemm_dgrad(dy, offsets, w, z=None, act="none", residual=None, dx=None, status=None, stream=None):
     """dx[r] = act'(z[r]) * (dy[r] w[e]) + residual[r]: the input gradient,
     through the activation x = act(z) that made the input when z [rows, k] is
     given. Returns dx [rows, k]."""
-    return _dgrad("moe_grouped_gemm_dgrad", 3, dy, _given(offsets), w, z, act, residual, dx, status, stream)
+    return _dgrad("moe_grouped_gemm_dgrad", 3, dy, _required(offsets, "offsets"), w, z, act, residual, dx, status,
+                  stream)
 
 
 def moe_grouped_gemm_wgrad(dy, offsets, x, dw=None, dbias=None, status=None, stream=None):
     """dw[e] = dy_e^T x_e (fp32 [E, n, k], E from offsets); dbias [E, n] fp32,
     when given, receives the column sums of dy_e. Returns dw."""
-    return _wgrad("moe_grouped_gemm_wgrad", 3, dy, _given(offsets), x, offsets.numel() - 1, dw, dbias, status, stream)
+    _axes(offsets, 1, "offsets")
+    groups = offsets.numel() - 1
+    if groups < 1:
+        raise ValueError("offsets: needs E + 1 entries")
+    return _wgrad("moe_grouped_gemm_wgrad", 3, dy, offsets, x, groups, dw, dbias, status, stream)
 
 
 def moe_linear(x, w, bias=None, act="none", residual=None, preact=None, y=None, status=None, stream=None):
@@ -698,10 +718,10 @@ def moe_linear_wgrad(dy, x, dw=None, dbias=None, status=None, stream=None):
     return _wgrad("moe_linear_wgrad", 2, dy, None, x, 1, dw, dbias, status, stream)
 
 
-def _given(offsets):
-    if offsets is None:
-        raise TypeError("offsets: expected a torch.Tensor")
-    return offsets
+def _required(t, name):
+    if t is None:
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return t
 
 
 _PRODUCTS = {"forward": MOE_PRODUCT_FORWARD, "dgrad": MOE_PRODUCT_DGRAD, "wgrad": MOE_PRODUCT_WGRAD}
@@ -726,7 +746,7 @@ def moe_act_backward(dy, z, act, dz=None, stream=None):
     dev, dt = _first(dy, 2, "dy")
     shape = dy.shape
     pdy, ldy = _strided(dy, shape, dy.dtype, dev, "dy")
-    pz, ldz = _strided(z, shape, dy.dtype, dev, "z")
+    pz, ldz = _strided(_required(z, "z"), shape, dy.dtype, dev, "z")
     if dz is None:
         dz = _matrix(*shape, dy.dtype, dy.device, stream)
     pdz, ldr = _strided(dz, shape, dy.dtype, dev, "dz")
@@ -764,8 +784,8 @@ def moe_unpermute_combine_dropout(cfg, y_perm, dest_row, topk_gate, p, rng=None,
     if y_perm.shape[0] < perm_rows(cfg) or y_perm.shape[1] != cfg.d:
         raise ValueError(f"y_perm: shape {tuple(y_perm.shape)}, needs {rows} rows of {cfg.d}")
     pp = _plain(y_perm, y_perm.shape, dt, dev, "y_perm")
-    pd = _plain(dest_row, (cfg.T, cfg.k), torch.int32, dev, "dest_row")
-    pg = _plain(topk_gate, (cfg.T, cfg.k), torch.float32, dev, "topk_gate")
+    pd = _plain(_required(dest_row, "dest_row"), (cfg.T, cfg.k), torch.int32, dev, "dest_row")
+    pg = _plain(_required(topk_gate, "topk_gate"), (cfg.T, cfg.k), torch.float32, dev, "topk_gate")
     pr = _plain(residual, (cfg.T, cfg.d), dt, dev, "residual")
     if y is None:
         y = _empty((cfg.T, cfg.d), dt, y_perm.device, stream)

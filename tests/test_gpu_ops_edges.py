@@ -384,3 +384,18 @@ def test_a_wait_that_runs_out_in_every_form(case):
     status.zero_()
     assert torch.equal(call(), ref)
     assert int(status.item()) == 0
+
+
+def test_binding_names_what_is_no_tensor():
+    x, w, o = torch.zeros((4, 16), device=DEV), torch.zeros((2, 8, 16), device=DEV), torch.tensor([0, 2, 4], device=DEV)
+    dy, cfg = torch.zeros((4, 8), device=DEV), M.config(2, 16, 4, 2, 128, "f32", "identity")
+    d, g = torch.zeros((2, 2), dtype=torch.int32, device=DEV), torch.zeros((2, 2), device=DEV)
+    for name, call in (("w", lambda: M.moe_linear(x, None)), ("w", lambda: M.moe_linear(x, [[0.0] * 16] * 8)),
+                       ("w", lambda: M.moe_linear_dgrad(dy, None)), ("offsets", lambda: M.moe_grouped_gemm(x, [0, 2, 4], w)),
+                       ("bias", lambda: M.moe_linear(x, w[0], bias=[0.0] * 8)), ("x", lambda: M.moe_linear_wgrad(dy, None)),
+                       ("residual", lambda: M.moe_linear(x, w[0], residual=1.0)), ("z", lambda: M.moe_act_backward(x, None, "relu")),
+                       ("status", lambda: M.moe_linear(x, w[0], status=0)), ("rng", lambda: M.moe_dropout(x, 0.5, [1, 2])),
+                       ("dest_row", lambda: M.moe_unpermute_combine_dropout(cfg, x, None, g, 0.0)),
+                       ("topk_gate", lambda: M.moe_unpermute_combine_dropout(cfg, x, d, None, 0.0))):
+        with pytest.raises(TypeError, match=f"^{name}: "):
+            call()

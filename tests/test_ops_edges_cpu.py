@@ -144,3 +144,15 @@ def test_stalled_cases_take_every_tiled_form(L):
     assert {(c[0], c[6]) for c in STALLS} >= {(p, f) for p, f in (
         ("forward", M.MOE_FORM_SINGLE), ("forward", M.MOE_FORM_PAIR), ("forward", M.MOE_FORM_SPLIT),
         ("dgrad", M.MOE_FORM_PAIR), ("dgrad", M.MOE_FORM_SPLIT), ("wgrad", M.MOE_FORM_PAIR), ("wgrad", M.MOE_FORM_SPLIT))}
+
+
+def test_what_is_no_tensor_is_a_type_error():
+    for check in (lambda t: _lib._strided(t, (2, 2), torch.float32, -1, "t"), lambda t: _lib._plain(t, (2, 2), torch.float32, -1, "t"),
+                  lambda t: _lib._axes(t, 2, "t"), lambda t: _lib._first(t, 2, "t")):
+        for t in ([[1.0, 2.0], [3.0, 4.0]], 3, torch.zeros(2, 2).numpy()):
+            with pytest.raises(TypeError, match="t: expected a torch.Tensor"):
+                check(t)
+    with pytest.raises(TypeError, match="z: "):
+        _lib._required(None, "z")
+    with pytest.raises(ValueError, match="offsets"):
+        M.moe_grouped_gemm_wgrad(torch.zeros(4, 8), torch.zeros(0, dtype=torch.int32), torch.zeros(4, 8))
