@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();  // every partial tile is in place
     if (warp >= 2 && first_tile < total && !*abort_flag) {
       const Tile c = tile_at(first_tile);
-        uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
+      uint8_t* stg = stg_all + (warp - 2) * S::kStgBytes;
       // the tile's blocks of 32 x 32 shared out over the cluster's epilogue warps
 #pragma unroll 1
       for (int b = rank * kEpiWarps + warp - 2; b < (a.bn / 32) * 4; b += split * kEpiWarps) {

@@ -457,7 +457,9 @@ MOE_API int32_t moe_debug_stall_next_gemms(int32_t n);
  * [rows, n] or NULL (may be y itself: same address and stride), preact
  * [rows, n] or NULL: receives u for the backward. offsets [groups + 1] int32
  * on the device. Groups may be empty; rows outside every group are left as
- * they were. Sums, bias, activation and residual are fp32, rounded once each
+ * they were. In the PADDED layout a group's rows include its padding rows:
+ * their outputs are those of zero rows (which nothing reads), and the
+ * gradients that enter _dgrad and _wgrad have to be zero on them. Sums, bias, activation and residual are fp32, rounded once each
  * to y and preact. fp32 products run on the CUDA cores in IEEE fp32, bf16
  * ones on tensor cores. No workspace. Deterministic.
  * No other operand may overlap an output.

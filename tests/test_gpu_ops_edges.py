@@ -399,3 +399,57 @@ def test_binding_names_what_is_no_tensor():
                        ("topk_gate", lambda: M.moe_unpermute_combine_dropout(cfg, x, d, None, 0.0))):
         with pytest.raises(TypeError, match=f"^{name}: "):
             call()
+
+
+@pytest.mark.parametrize("case", [c for c in FORMS if c[0] != "wgrad"], ids=name_of)
+def test_a_residual_in_place_in_every_form(case):
+    """residual = y (dx), the same buffer: each element is read before it is written, whichever kernel runs."""
+    product, dt, sizes, n, k, pad = case[:6]
+    g, dense, ends, rows, E, o, x, dy = product_setup(case)
+    w = integers((E, n, k), dt, g, pad)
+    forward = product == "forward"
+    res = integers((rows, n if forward else k), dt, g, pad)
+    z = integers((rows, k), dt, g, pad, 1)
+    inside = slice(ends[0], ends[-1])
+
+    def call(residual, out):
+        if forward:
+            return M.moe_grouped_gemm(x, o, w, act="silu", residual=residual, y=out)[inside]
+        return M.moe_grouped_gemm_dgrad(dy, o, w, z=z, act="silu", residual=residual, dx=out)[inside]
+
+    apart = call(res, integers((rows, res.shape[1]), dt, g, pad)).clone()
+    assert torch.equal(call(res, res), apart)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_experts_over_the_padded_layout(dt):
+    """The fixed-capacity layout: its padding rows (zero in x_perm) belong to the groups. The experts' outputs there
+    are those of zero rows and nothing reads them; gradients that are zero there add nothing to dw and dbias, exactly
+    as without padding (whole numbers)."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    T, d, E, k, F, cap = 203, 128, 8, 2, 136, 40
+    h, wr = integers((T, d), dt, g), torch.randn((E, d), generator=g, device=DEV).to(dt)
+    w1, b1 = integers((E, F, d), dt, g), torch.randint(-9, 10, (E, F), generator=g, device=DEV).float()
+    outs = []
+    for layout in ("compact", "padded"):
+        cfg = M.config(T, d, E, k, 128, dt, "identity", capacity=cap, layout=layout)
+        idx, gate = M.moe_route(cfg, h, wr)
+        pm = M.moe_permute(cfg, h, idx)
+        y = M.moe_grouped_gemm(pm["x_perm"], pm["offsets"], w1, bias=b1, act="relu")
+        dest = pm["dest_row"].reshape(-1).long()
+        kept = dest >= 0
+        dy = torch.zeros_like(y)
+        dy[dest[kept]] = (torch.arange(T * k, device=DEV)[kept, None] % 5 - 2).to(dt).expand(-1, F)
+        db = torch.empty((E, F), device=DEV)
+        dw = M.moe_grouped_gemm_wgrad(dy, pm["offsets"], pm["x_perm"], dbias=db)
+        dx = M.moe_grouped_gemm_dgrad(dy, pm["offsets"], w1)
+        if layout == "padded":
+            assert pm["offsets"].tolist() == [e * cap for e in range(E + 1)]
+            used = torch.zeros(E * cap, dtype=torch.bool, device=DEV)
+            used[dest[kept]] = True
+            assert bool(kept.any()) and not bool(used.all())
+            exactly(y[~used], b1.repeat_interleave(cap, 0)[~used].clamp(min=0), "padding rows")
+            assert not dx[~used].any()
+        outs.append((kept, y[dest[kept]], dw, db, dx[dest[kept]]))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
