@@ -214,8 +214,20 @@ cudaError_t launch_features(const MatmulArgs& a, long long blocks, cudaStream_t 
 static long long row_blocks(const MatmulArgs& a) { return (a.rows + 7LL) / 8 + std::min(a.groups, a.rows) - 1; }
 
 // Where this kernel measured faster than the tiles (us, here / there):
-//  - one block a group: k 4096, n 14336, 1-8 rows 24.1 / 28.1; k 1408, n 2048
-//    3.5 / 8.5; 2 tokens of 8 experts each out of 128 13.4 / 26.1;
+//  - one block of one group: k 4096, n 14336, 1-8 rows 24.1 / 28.1; k 1408, n 2048
+//    3.5 / 8.5;
+//  - at most half as many rows as groups, so mostly a group's weights for each
+//    row. In captured loops over weights that leave L2, k 2048 (rows of random
+//    routes; past the cut in brackets, where the tiles run):
+//      groups, n  |  rows 8        16           32           64           128
+//      128,  768  |  7.3 / 15.9  11.6 / 26.0  23.8 / 22.6  37.9 / 35.3  [50.4 / 44.2]
+//      256,  768  |  8.6 / 19.2  13.4 / 27.8  25.6 / 23.0  39.8 / 36.1   64.8 / 62.4
+//      64,  1408  |  9.2 / 21.5  15.9 / 33.6  29.4 / 44.3 [47.8 / 43.0] [66.0 / 60.9]
+//    (6, 12, 30, 60 and 126 rows in the last line); k 768, n 2048, 128 groups:
+//    8.1 / 17.6, 15.2 / 19.3, 26.0 / 24.3, 43.0 / 35.8, [60.0 / 44.6]. So the cut
+//    lies too far for 128 groups and more, by 5 to 20% of a call between a
+//    quarter and a half, and too near for 64; the crossing follows the tiles'
+//    widths more than the rows;
 //  - several blocks that read a group's weights again from L2, while all of
 //    them run at once: on half of the SMs' warps k = n = 4096, 16 rows
 //    11.2 / 13.7, k 2048, n 16, 2048 rows 3.8 / 9.9 (k 128, n 640, 256 rows, more

@@ -72,7 +72,7 @@ extern "C" {
 #define MOE_STATUS_NAN_LOGIT 1  /* a router logit was NaN (treated as -inf) */
 #define MOE_STATUS_BAD_ROUTE 2  /* an index out of [0,E) or repeated within a token (slot dropped) */
 #define MOE_STATUS_TIMEOUT   4  /* a bounded on-chip wait gave up (output invalid) */
-#define MOE_STATUS_BAD_OFFSETS 32 /* group offsets that fall or leave [0, rows] (clamped; those groups' outputs are
+#define MOE_STATUS_BAD_OFFSETS 32 /* group offsets that fall or leave [0, rows] (clamped; the call's outputs are
                                      invalid, nothing outside the buffers is touched) */
 /* MXFP8 precision only, informational (the output is valid): */
 #define MOE_STATUS_MX_SATURATED 8   /* an element was clamped to +-448 when quantised; the OCP scale
