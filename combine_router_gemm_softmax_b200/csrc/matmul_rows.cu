@@ -225,9 +225,9 @@ static long long row_blocks(const MatmulArgs& a) { return (a.rows + 7LL) / 8 + s
 //      64,  1408  |  9.2 / 21.5  15.9 / 33.6  29.4 / 44.3 [47.8 / 43.0] [66.0 / 60.9]
 //    (6, 12, 30, 60 and 126 rows in the last line); k 768, n 2048, 128 groups:
 //    8.1 / 17.6, 15.2 / 19.3, 26.0 / 24.3, 43.0 / 35.8, [60.0 / 44.6]. So the cut
-//    lies too far for 128 groups and more, by 5 to 20% of a call between a
-//    quarter and a half, and too near for 64; the crossing follows the tiles'
-//    widths more than the rows;
+//    lies about right for 64 groups (48 rows 39.8 / 40.9, 96 rows 56.0 / 58.6)
+//    and too far for 128 and more, by 5 to 20% of a call between a quarter and
+//    a half; the crossing follows the tiles' widths more than the rows;
 //  - several blocks that read a group's weights again from L2, while all of
 //    them run at once: on half of the SMs' warps k = n = 4096, 16 rows
 //    11.2 / 13.7, k 2048, n 16, 2048 rows 3.8 / 9.9 (k 128, n 640, 256 rows, more

@@ -10,7 +10,10 @@
 // microsecond of arithmetic, four for 64-wide ones, whose slice takes a
 // quarter of the load latency). Operands are read as they lie: along the
 // reduction or across it, by template, so no mode needs a transposed copy.
-// Bound: the fp32 pipe (128 multiply-adds a cycle and SM).
+// Bound: the fp32 pipe (128 multiply-adds a cycle and SM) for 128-wide tiles;
+// for 64-wide ones the shared-memory loads, two of 16 bytes for a thread's
+// eight packed multiply-adds (333 x 768 x 1000: 26.8 us, L1 73% busy, the fp32
+// pipe 22%).
 //
 // Few tiles leave SMs idle, so a cluster of S CTAs can share one 64 x 64 tile:
 // each takes a part of the reduction, and the partial tiles are added through
