@@ -242,7 +242,10 @@ int32_t moe_product_form_used(const moe_gemm_config* cfg, int32_t product, int32
 }
 
 int32_t moe_act_backward(const moe_gemm_config* cfg, const void* dy, const void* z, void* dz, moe_stream_t stream) {
-  const Product p = check(cfg, true, {false, false, true, cfg ? cfg->n : 0, cfg ? cfg->n : 0});
+  if (cfg == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_gemm_config matrix = *cfg;
+  matrix.k = matrix.groups = 1;  // no product: neither counts
+  const Product p = check(&matrix, true, {false, false, true, cfg->n, cfg->n});
   if (p.rc != MOE_OK) return p.rc;
   const moe_gemm_config& c = p.c;
   if (c.rows > 0 && (!dy || !z || !dz)) return MOE_ERR_INVALID_ARG;

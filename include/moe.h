@@ -520,7 +520,8 @@ MOE_API int32_t moe_product_form_used(const moe_gemm_config* cfg, int32_t produc
 
 /* moe_act_backward -- dz[r, j] = dy[r, j] act'(z[r, j]) over [rows, n], for an
  * activation whose output no further product consumes (else
- * moe_*_dgrad applies it). dy: stride ldy, z: ldz, dz: ldr (0: n). dz may be dy. */
+ * moe_*_dgrad applies it). dy: stride ldy, z: ldz, dz: ldr (0: n). dz may be
+ * dy. cfg's k and groups are not looked at. */
 MOE_API int32_t moe_act_backward(const moe_gemm_config* cfg, const void* dy, const void* z, void* dz,
                                  moe_stream_t stream);
 

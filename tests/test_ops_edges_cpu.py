@@ -156,3 +156,10 @@ def test_what_is_no_tensor_is_a_type_error():
         _lib._required(None, "z")
     with pytest.raises(ValueError, match="offsets"):
         M.moe_grouped_gemm_wgrad(torch.zeros(4, 8), torch.zeros(0, dtype=torch.int32), torch.zeros(4, 8))
+
+
+def test_act_backward_needs_no_product_sizes(L):
+    cfg = M.MoeGemmConfig(rows=0, n=8, dtype=M.MOE_DTYPE_F32, act=M.MOE_ACT_SILU)  # k and groups left at zero
+    assert L.moe_act_backward(cfg, None, None, None, None) == M.MOE_OK
+    assert L.moe_act_backward(M.MoeGemmConfig(rows=4, n=8, act=9), PTR, PTR, PTR, None) == M.MOE_ERR_INVALID_ARG
+    assert L.moe_act_backward(M.MoeGemmConfig(rows=4, n=0), PTR, PTR, PTR, None) == M.MOE_ERR_INVALID_ARG
