@@ -453,3 +453,16 @@ def test_experts_over_the_padded_layout(dt):
         outs.append((kept, y[dest[kept]], dw, db, dx[dest[kept]]))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("act", R.ACTS)
+def test_activations_of_nan_and_infinity(act, dt):
+    """NaN in a token's row makes all of its outputs NaN and no other token's; plus infinity stays what it is."""
+    for rows in (3, 700):
+        x = torch.ones((rows, 8), dtype=dt, device=DEV)
+        x[0, 3], x[1] = math.nan, math.inf
+        y = M.moe_linear(x, torch.ones((16, 8), dtype=dt, device=DEV), act=act)
+        assert bool(y[0].isnan().all()) and bool((y[1] == math.inf).all())
+        exactly(y[2:], torch.full((rows - 2, 16), 8.0, device=DEV).to(dt).float(), act) if act in ("none", "relu") else None
+        assert bool(y[2:].isfinite().all())
