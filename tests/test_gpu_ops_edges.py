@@ -466,3 +466,28 @@ def test_activations_of_nan_and_infinity(act, dt):
         assert bool(y[0].isnan().all()) and bool((y[1] == math.inf).all())
         exactly(y[2:], torch.full((rows - 2, 16), 8.0, device=DEV).to(dt).float(), act) if act in ("none", "relu") else None
         assert bool(y[2:].isfinite().all())
+
+
+def test_a_captured_fork_makes_its_outputs():
+    """Calls on a second stream of a capture, with outputs made and dropped there, replayed twice beside other work."""
+    calls = calls_on_a_stream()
+    refs = {name: call(None).clone() for name, call in calls.items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    got = {}
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        for name, call in calls.items():
+            call(side)  # its output is dropped at once
+            got[name] = call(side)
+        main.wait_stream(side)
+        beside = calls["linear"](None)
+    for _ in range(2):
+        graph.replay()
+        torch.full_like(beside, 3.0)
+    torch.cuda.synchronize()
+    for name, y in got.items():
+        assert torch.equal(y, refs[name]), name
+    assert torch.equal(beside, refs["linear"])
